@@ -1,7 +1,7 @@
 """MI355X-native LFM2 gated short causal convolution (ShortConv).
 
 The computation lives in liblfm2sc.so (hand-written HIP kernels for gfx950
-behind the C ABI of include/lfm2sc.h); this package only loads it and
+behind the C ABI of include/lfm2sc.h and include/lfm2sc_hybrid.h); this package only loads it and
 marshals torch tensors into its calls.  Build the library with
 ``python -m gated_short_causal_amd.build``.
 """
@@ -21,4 +21,13 @@ from .binding import (  # noqa: F401
     lfm2sc_fused_prefill_workspace_bytes,
     lfm2sc_prefill_ragged,
     lfm2sc_verify_window,
+)
+from .hybrid import (  # noqa: F401
+    lfm2sc_accept_drafts,
+    lfm2sc_accept_drafts_workspace_bytes,
+    lfm2sc_attn_backward,
+    lfm2sc_attn_backward_workspace_bytes,
+    lfm2sc_attn_cached,
+    lfm2sc_attn_cached_workspace_bytes,
+    lfm2sc_attn_prefill,
 )

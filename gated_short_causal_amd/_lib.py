@@ -42,7 +42,24 @@ SIGNATURES = {
     "lfm2sc_abi_version": (_int, []),
 }
 
+# the same for include/lfm2sc_hybrid.h
+_f32 = ctypes.c_float
+HYBRID_SIGNATURES = {
+    "lfm2sc_attn_prefill": (_int, [_int, _int, _int, _int, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _int, _f32, _vp,
+                                   _i64, _vp, _vp]),
+    "lfm2sc_attn_backward_workspace_bytes": (_size, [_int, _int, _int, _int, _i64, _int]),
+    "lfm2sc_attn_backward": (_int, [_int, _int, _int, _int, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _int, _f32, _vp,
+                                    _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _size, _vp]),
+    "lfm2sc_attn_cached_workspace_bytes": (_size, [_int, _int, _int, _int, _int, _int, _int, _int, _int]),
+    "lfm2sc_attn_cached": (_int, [_int, _int, _int, _int, _vp, _i64, _int, _int, _vp, _vp, _i64, _int, _int, _vp, _int,
+                                  _vp, _int, _vp, _f32, _vp, _i64, _vp, _size, _vp]),
+    "lfm2sc_accept_drafts_workspace_bytes": (_size, [_int, _int, _int]),
+    "lfm2sc_accept_drafts": (_int, [_int, _int, _int, _int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                    _size, _vp]),
+}
+
 _lib = None
+_hybrid = None
 
 
 def lib():
@@ -61,3 +78,16 @@ def lib():
         fn.argtypes = args
     _lib = handle
     return handle
+
+
+def hybrid_lib():
+    """lib(), with the entry points of include/lfm2sc_hybrid.h typed as well (a library without them raises)."""
+    global _hybrid
+    if _hybrid is None:
+        handle = lib()
+        for name, (res, args) in HYBRID_SIGNATURES.items():
+            fn = getattr(handle, name)
+            fn.restype = res
+            fn.argtypes = args
+        _hybrid = handle
+    return _hybrid

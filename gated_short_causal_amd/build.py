@@ -15,7 +15,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblfm2sc.so")
-SOURCES = ["fwd.hip", "bwd.hip", "fused.hip", "fused_split.hip", "interop.hip", "check.hip", "noalloc.hip", "api.cpp"]
+SOURCES = ["fwd.hip", "bwd.hip", "fused.hip", "fused_split.hip", "interop.hip", "check.hip", "noalloc.hip", "api.cpp",
+           "attn_fwd.hip", "attn_bwd.hip", "attn_cached.hip", "drafts.hip", "api_hybrid.cpp"]
 
 
 def hipcc() -> str:

@@ -8,17 +8,15 @@
 
 #include <cstdarg>
 #include <cstdio>
-#include <cstdlib>
 #include <cstring>
 
+#include "api_common.hpp"
 #include "fused_common.hpp"
 #include "kernels.hpp"
 
-namespace {
+namespace lfm2sc {
 
-using namespace lfm2sc;
-
-thread_local char g_err[512] = "";
+static thread_local char g_err[512] = "";
 
 int fail(int code, const char* fmt, ...) {
     va_list ap;
@@ -33,24 +31,13 @@ int ok() {
     return LFM2SC_OK;
 }
 
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+}  // namespace lfm2sc
 
-bool check_mode() {
-    static const bool on = [] {
-        const char* e = std::getenv("LFM2SC_CHECK");
-        return e != nullptr && e[0] == '1';
-    }();
-    return on;
-}
+namespace {
+
+using namespace lfm2sc;
 
 constexpr int kMaxH = 1 << 20;
-constexpr int64_t kMaxRows = (int64_t)1 << 31;   // row offsets are int32
-
-#define TRY(expr)                       \
-    do {                                \
-        const int rc_ = (expr);         \
-        if (rc_ != LFM2SC_OK) return rc_; \
-    } while (0)
 
 int check_common(const char* fn, int dtype, int H, int K, const void* bias) {
     if (dtype != LFM2SC_BF16 && dtype != LFM2SC_F32)
@@ -63,21 +50,6 @@ int check_common(const char* fn, int dtype, int H, int K, const void* bias) {
     return LFM2SC_OK;
 }
 
-int check_stride(const char* fn, const char* name, int64_t stride, int64_t min) {
-    if (stride < min) return fail(LFM2SC_ERR_BAD_SHAPE, "%s: %s=%lld is below the minimum %lld", fn, name,
-                                  (long long)stride, (long long)min);
-    if (stride % 8 != 0) return fail(LFM2SC_ERR_ALIGNMENT, "%s: %s=%lld is not a multiple of 8 elements", fn, name,
-                                     (long long)stride);
-    return LFM2SC_OK;
-}
-
-int check_ptr(const char* fn, const char* name, const void* p, uintptr_t align) {
-    if (p == nullptr) return fail(LFM2SC_ERR_NULL_POINTER, "%s: %s is NULL", fn, name);
-    if (!aligned(p, align)) return fail(LFM2SC_ERR_ALIGNMENT, "%s: %s=%p is not %u-byte aligned", fn, name, p,
-                                        (unsigned)align);
-    return LFM2SC_OK;
-}
-
 int check_pool(const char* fn, const void* pool, int64_t num_slots, int64_t slot_stride, const int32_t* slot_idx,
                int H, int K) {
     TRY(check_ptr(fn, "state_pool", pool, 16));
@@ -85,11 +57,6 @@ int check_pool(const char* fn, const void* pool, int64_t num_slots, int64_t slot
     if (num_slots < 1) return fail(LFM2SC_ERR_BAD_SHAPE, "%s: num_slots=%lld must be >= 1", fn, (long long)num_slots);
     TRY(check_stride(fn, "slot_stride", slot_stride, (int64_t)H * K));
     return LFM2SC_OK;
-}
-
-int launched(const char* fn, hipError_t e) {
-    if (e != hipSuccess) return fail(LFM2SC_ERR_HIP, "%s: HIP error %d (%s)", fn, (int)e, hipGetErrorString(e));
-    return ok();
 }
 
 int device_check(const char* fn, hipStream_t s, const int32_t* slot_idx, int N, int64_t num_slots, const int32_t* cu,
@@ -263,7 +230,7 @@ extern "C" {
 
 int lfm2sc_abi_version(void) { return LFM2SC_ABI_VERSION; }
 
-const char* lfm2sc_last_error(void) { return g_err; }
+const char* lfm2sc_last_error(void) { return lfm2sc::g_err; }
 
 const char* lfm2sc_status_string(int status) {
     switch (status) {

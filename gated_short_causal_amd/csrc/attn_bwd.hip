@@ -1,0 +1,274 @@
+// attn_bwd.hip -- backward of the causal attention over packed prompts.
+//
+// With p = exp(scale s - lse) and delta[t] = sum_d dout[t][d] out[t][d]:
+//   dv[j] = sum_t p[t][j] dout[t]        ds[t][j] = p[t][j] (dout[t].v[j] - delta[t])
+//   dk[j] = scale sum_t ds[t][j] q[t]    dq[t] = scale sum_j ds[t][j] k[j]
+// where the sums over t of dk and dv run over every query head of the group.
+//
+// Two passes over the score blocks, neither with atomics, so the gradients are
+// the same bits every time: one by key blocks (dk, dv stay in registers while
+// the group's heads and queries stream past), one by query blocks (dq stays,
+// keys stream).  Both form p again from q, k and lse.
+#include "attn_common.hpp"
+#include "hybrid.hpp"
+
+namespace lfm2sc {
+
+// delta and lse in base 2, [Hq][total_T] each.  D / 8 lanes hold one head of a
+// row; a wave does 8 consecutive rows, after which lane j of those lanes
+// (j < 8) writes row j.
+template <int D>
+__global__ __launch_bounds__(256) void attn_delta_kernel(AttnGradArgs a) {
+    constexpr int kLanes = D / 8;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t t0 = ((int64_t)blockIdx.x * 4 + wave) * 8;
+    const int head = blockIdx.y * (64 / kLanes) + lane / kLanes, j = lane % kLanes;
+    if (t0 >= a.f.total_T || head >= a.f.Hq) return;
+    float mine = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        float s = 0.f;
+        if (t0 + r < a.f.total_T) {
+            float x[8], y[8];
+            load_f32x8<uint16_t>(a.dout + (t0 + r) * a.dout_stride + head * D + 8 * j, x);
+            load_f32x8<uint16_t>(a.f.out + (t0 + r) * a.f.out_stride + head * D + 8 * j, y);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = __builtin_fmaf(x[i], y[i], s);
+        }
+#pragma unroll
+        for (int d = 1; d < kLanes; d <<= 1) s += __shfl_xor(s, d, 64);
+        if (j == r) mine = s;
+    }
+    const int64_t t = t0 + j;
+    if (j < 8 && t < a.f.total_T) {
+        const int64_t at = (int64_t)head * a.f.total_T + t;
+        a.delta[at] = mine;
+        a.lse2[at] = a.f.lse[at] * kLog2e;
+    }
+}
+
+// dk and dv: a wave owns 32 keys, a workgroup 32 W consecutive ones.  Two
+// stages of query tiles (q rows, dout rows) and their lse and delta in LDS.
+template <int D, int W>
+__device__ __forceinline__ void dkv_part(const AttnGradArgs& a, uint8_t* qb0, uint8_t* db0, uint8_t* qb1, uint8_t* db1,
+                                         float* lb0, float* eb0, float* lb1, float* eb1, int block, int wave, int lane) {
+    using T = Tile<D>;
+    constexpr int kBN = 32 * W;
+    const int c = lane & 31, h = lane >> 5;
+    const AttnArgs& f = a.f;
+    const int G = f.Hq / f.Hkv;
+    const int kvh = block % f.Hkv;
+    const SeqTile st = find_seq_tile<false>(f.cu, f.N, f.total_T, block / f.Hkv, kBN);
+    if (st.len == 0) return;
+    const int n0 = st.block * kBN;
+    const int wkey = n0 + wave * 32;
+    const int first = n0 / 64, last = (st.len + 63) / 64;     // query tiles [first, last) of 64 rows
+    const int per_head = last - first, steps = per_head * G;
+
+    const TileCopy<D, W> qcopy(wave, lane, f.q_stride), dcopy(wave, lane, a.dout_stride);
+    auto issue = [&](uint8_t* qb, uint8_t* db, float* lb, float* eb, int step) {
+        const int head = kvh * G + step / per_head, t = first + step % per_head;
+        const int rows = min(64, st.len - t * 64);
+        const int64_t row = st.start + (int64_t)t * 64;
+        qcopy(f.q + row * f.q_stride + (int64_t)head * D, f.q_stride, rows, qb, wave);
+        dcopy(a.dout + row * a.dout_stride + (int64_t)head * D, a.dout_stride, rows, db, wave);
+        if (wave == 0) {
+            const int64_t at = (int64_t)head * f.total_T + row;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_rsrc(a.lse2 + at, rows * 4), (lds_ptr_t)lb, 4, lane * 4, 0, 0, 0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_rsrc(a.delta + at, rows * 4), (lds_ptr_t)eb, 4, lane * 4, 0, 0, 0);
+        }
+    };
+    issue(qb0, db0, lb0, eb0, 0);
+
+    bf16x8 kf[D / 16], vf[D / 16];
+    const bool exists = wkey + c < st.len;
+    const int64_t krow = st.start + wkey + c;
+    load_row_operand<D>(kf, f.k + krow * f.k_stride + (int64_t)kvh * D, h, exists);
+    load_row_operand<D>(vf, f.v + krow * f.v_stride + (int64_t)kvh * D, h, exists);
+    const LaneOffsets<D> lo(lane);
+    const float cs = f.scale * kLog2e;
+    f32x16 dk[D / 32], dv[D / 32];
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dk[b][i] = dv[b][i] = 0.f;
+
+    auto tile = [&](const uint8_t* qb, const uint8_t* db, const float* lb, const float* eb, int t) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {            // 32 query rows at a time
+            const int r0 = t * 64 + n * 32;
+            if (r0 + 31 < wkey) continue;        // all before the wave's keys
+            f32x16 s, e;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = e[i] = 0.f;
+#pragma unroll
+            for (int ds = 0; ds < D / 16; ++ds) {
+                s = mfma32(lds_row(qb + n * 32 * T::kRowB, lo.row[ds]), kf[ds], s);
+                e = mfma32(lds_row(db + n * 32 * T::kRowB, lo.row[ds]), vf[ds], e);
+            }
+            f32x16 lse, del;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 x = *reinterpret_cast<const float4*>(lb + n * 32 + 8 * j + 4 * h);
+                const float4 y = *reinterpret_cast<const float4*>(eb + n * 32 + 8 * j + 4 * h);
+                lse[4 * j] = x.x; lse[4 * j + 1] = x.y; lse[4 * j + 2] = x.z; lse[4 * j + 3] = x.w;
+                del[4 * j] = y.x; del[4 * j + 1] = y.y; del[4 * j + 2] = y.z; del[4 * j + 3] = y.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = exp2_fast(__builtin_fmaf(s[i], cs, -lse[i]));
+            if (r0 < wkey + 31) {
+                const int key = wkey + c - r0 - 4 * h;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if ((i & 3) + 8 * (i >> 2) < key) s[i] = 0.f;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) e[i] = s[i] * (e[i] - del[i]);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16x8 p = to_operand(s, ks), g = to_operand(e, ks);
+                const int at = (n * 32 + ks * 16) * T::kRowB;
+#pragma unroll
+                for (int b = 0; b < D / 32; ++b) {
+                    dv[b] = mfma32(lds_transposed(db + at, lo.tr[0][b], lo.tr[1][b]), p, dv[b]);
+                    dk[b] = mfma32(lds_transposed(qb + at, lo.tr[0][b], lo.tr[1][b]), g, dk[b]);
+                }
+            }
+        }
+    };
+    auto step = [&](const uint8_t* qb, const uint8_t* db, const float* lb, const float* eb, uint8_t* qn, uint8_t* dn,
+                    float* ln, float* en, int i) {
+        wait_vm<0>();
+        stage_barrier();
+        if (i + 1 < steps) issue(qn, dn, ln, en, i + 1);
+        if (wkey < st.len) tile(qb, db, lb, eb, first + i % per_head);
+    };
+    for (int i = 0; i < steps; i += 2) {
+        step(qb0, db0, lb0, eb0, qb1, db1, lb1, eb1, i);
+        if (i + 1 < steps) step(qb1, db1, lb1, eb1, qb0, db0, lb0, eb0, i + 1);
+    }
+    store_transposed<D>(a.dk + krow * a.dk_stride + (int64_t)kvh * D, dk, f.scale, h, exists);
+    store_transposed<D>(a.dv + krow * a.dv_stride + (int64_t)kvh * D, dv, 1.f, h, exists);
+}
+
+// dq: a wave owns 32 query rows of one head, a workgroup 32 W consecutive ones.
+template <int D, int W>
+__device__ __forceinline__ void dq_part(const AttnGradArgs& a, uint8_t* kb0, uint8_t* vb0, uint8_t* kb1, uint8_t* vb1,
+                                        int block, int wave, int lane) {
+    using T = Tile<D>;
+    constexpr int kBM = 32 * W;
+    const int c = lane & 31, h = lane >> 5;
+    const AttnArgs& f = a.f;
+    const int G = f.Hq / f.Hkv;
+    const int kvh = block % f.Hkv, head = kvh * G + (block / f.Hkv) % G;
+    const SeqTile st = find_seq_tile<true>(f.cu, f.N, f.total_T, block / f.Hq, kBM);
+    if (st.len == 0) return;
+    const int q0 = st.block * kBM;
+    const int wrow = q0 + wave * 32;
+    const int tiles = (min(q0 + kBM, st.len) + 63) / 64;
+
+    const uint16_t* kp = f.k + st.start * f.k_stride + (int64_t)kvh * D;
+    const uint16_t* vp = f.v + st.start * f.v_stride + (int64_t)kvh * D;
+    const TileCopy<D, W> kcopy(wave, lane, f.k_stride), vcopy(wave, lane, f.v_stride);
+    auto issue = [&](uint8_t* kb, uint8_t* vb, int t) {
+        const int rows = min(64, st.len - t * 64);
+        kcopy(kp + (int64_t)t * 64 * f.k_stride, f.k_stride, rows, kb, wave);
+        vcopy(vp + (int64_t)t * 64 * f.v_stride, f.v_stride, rows, vb, wave);
+    };
+    issue(kb0, vb0, 0);
+
+    bf16x8 qf[D / 16], df[D / 16];
+    const bool exists = wrow + c < st.len;
+    const int64_t row = st.start + wrow + c;
+    load_row_operand<D>(qf, f.q + row * f.q_stride + (int64_t)head * D, h, exists);
+    load_row_operand<D>(df, a.dout + row * a.dout_stride + (int64_t)head * D, h, exists);
+    float lse = 0.f, del = 0.f;
+    if (exists) {
+        lse = a.lse2[(int64_t)head * f.total_T + row];
+        del = a.delta[(int64_t)head * f.total_T + row];
+    }
+    const LaneOffsets<D> lo(lane);
+    const float cs = f.scale * kLog2e;
+    f32x16 dq[D / 32];
+#pragma unroll
+    for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) dq[x][i] = 0.f;
+
+    auto tile = [&](const uint8_t* kb, const uint8_t* vb, int t) {
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int k0 = t * 64 + n * 32;
+            if (k0 > wrow + 31) continue;
+            f32x16 s, e;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = e[i] = 0.f;
+#pragma unroll
+            for (int ds = 0; ds < D / 16; ++ds) {
+                s = mfma32(lds_row(kb + n * 32 * T::kRowB, lo.row[ds]), qf[ds], s);
+                e = mfma32(lds_row(vb + n * 32 * T::kRowB, lo.row[ds]), df[ds], e);
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[i] = exp2_fast(__builtin_fmaf(s[i], cs, -lse)) * (e[i] - del);
+            if (k0 + 31 > wrow) {
+                const int r = wrow + c - k0 - 4 * h;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if ((i & 3) + 8 * (i >> 2) > r) s[i] = 0.f;
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16x8 g = to_operand(s, ks);
+                const int at = (n * 32 + ks * 16) * T::kRowB;
+#pragma unroll
+                for (int x = 0; x < D / 32; ++x)
+                    dq[x] = mfma32(lds_transposed(kb + at, lo.tr[0][x], lo.tr[1][x]), g, dq[x]);
+            }
+        }
+    };
+    const int last = min(wrow + 32, st.len) - 1;
+    auto step = [&](const uint8_t* kb, const uint8_t* vb, uint8_t* kn, uint8_t* vn, int t) {
+        wait_vm<0>();
+        stage_barrier();
+        if (t + 1 < tiles) issue(kn, vn, t + 1);
+        if (t * 64 <= last && wrow < st.len) tile(kb, vb, t);
+    };
+    for (int t = 0; t < tiles; t += 2) {
+        step(kb0, vb0, kb1, vb1, t);
+        if (t + 1 < tiles) step(kb1, vb1, kb0, vb0, t + 1);
+    }
+    store_transposed<D>(a.dq + row * a.dq_stride + (int64_t)head * D, dq, f.scale, h, exists);
+}
+
+// Both kinds of workgroup in one launch, the key blocks first: they run
+// longest (a group's heads one after the other), and the query blocks fill in
+// behind them.
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, D == 64 ? 2 : 1) void attn_grad_kernel(AttnGradArgs a, int dkv_blocks) {
+    constexpr int kTileB = 64 * Tile<D>::kRowB;
+    __shared__ __attribute__((aligned(1024))) uint8_t x0[kTileB], y0[kTileB], x1[kTileB], y1[kTileB];
+    __shared__ __attribute__((aligned(1024))) float l0[64], e0[64], l1[64], e1[64];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    if ((int)blockIdx.x < dkv_blocks) dkv_part<D, W>(a, x0, y0, x1, y1, l0, e0, l1, e1, blockIdx.x, wave, lane);
+    else dq_part<D, W>(a, x0, y0, x1, y1, blockIdx.x - dkv_blocks, wave, lane);
+}
+
+template <int D, int W>
+static hipError_t launch_bwd(const AttnGradArgs& a, hipStream_t s) {
+    const AttnArgs& f = a.f;
+    const int64_t per_row = f.total_T / (32 * W) + f.N;
+    if (per_row * (f.Hkv + f.Hq) >= ((int64_t)1 << 31) || f.total_T / 32 >= ((int64_t)1 << 31) - 1) return hipErrorInvalidConfiguration;
+    const int heads = 64 / (D / 8);
+    hipLaunchKernelGGL((attn_delta_kernel<D>), dim3((uint32_t)((f.total_T + 31) / 32), (f.Hq + heads - 1) / heads), dim3(256),
+                       0, s, a);
+    hipLaunchKernelGGL((attn_grad_kernel<D, W>), dim3((uint32_t)(per_row * (f.Hkv + f.Hq))), dim3(64 * W), 0, s, a,
+                       (int)(per_row * f.Hkv));
+    return hipGetLastError();
+}
+
+hipError_t launch_attn_backward(const AttnGradArgs& a, int D, hipStream_t s) {
+    return D == 64 ? launch_bwd<64, 4>(a, s) : launch_bwd<128, 4>(a, s);
+}
+
+}  // namespace lfm2sc

@@ -1,0 +1,171 @@
+// attn_fwd.hip -- causal attention over packed prompts, grouped heads.
+//
+// One pass over the keys with the running maximum m and sum l of each query
+// row's softmax.  A wave owns 32 QB query rows of one head; a workgroup's W
+// waves own consecutive rows and share the K and V tiles (64 keys) that are
+// copied to LDS ahead of use.  Scores are formed transposed, S^T = K Q^T, so
+// that a lane holds 16 keys of one query per 32-key block: the row maximum and
+// sum are in-lane up to one exchange between the wave's halves, and
+// P^T = exp(S^T - m), rounded to bf16, is in place as the operand of
+// O^T += V^T P^T.  P never leaves the registers.
+#include "attn_common.hpp"
+#include "hybrid.hpp"
+
+namespace lfm2sc {
+
+constexpr int kKT = 64;     // keys per staged tile
+
+template <int D, int QB, int W>
+__global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a) {
+    using T = Tile<D>;
+    constexpr int kBM = 32 * QB * W;
+    constexpr int kTileB = kKT * T::kRowB;
+    __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[kTileB], kbuf1[kTileB], vbuf0[kTileB], vbuf1[kTileB];
+
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
+    // block -> (row block, head): all heads of a row block together, the key/value heads dealt to the XCDs in
+    // turn, so the heads that share keys and values run on the same XCDs
+    const int G = a.Hq / a.Hkv;
+    const int b = blockIdx.x;
+    const int kvh = b % a.Hkv, head = kvh * G + (b / a.Hkv) % G;
+    const SeqTile st = find_seq_tile<true>(a.cu, a.N, a.total_T, b / a.Hq, kBM);
+    if (st.len == 0) return;
+    const int q0 = st.block * kBM;
+    const int wrow = q0 + wave * 32 * QB;        // the wave's first row in the sequence
+    const int tiles = (min(q0 + kBM, st.len) + kKT - 1) / kKT;
+
+    const uint16_t* kp = a.k + st.start * a.k_stride + (int64_t)kvh * D;
+    const uint16_t* vp = a.v + st.start * a.v_stride + (int64_t)kvh * D;
+    const TileCopy<D, W> kcopy(wave, lane, a.k_stride), vcopy(wave, lane, a.v_stride);
+    auto issue = [&](uint8_t* kb, uint8_t* vb, int t) {
+        const int rows = min(kKT, st.len - t * kKT);
+        kcopy(kp + (int64_t)t * kKT * a.k_stride, a.k_stride, rows, kb, wave);
+        vcopy(vp + (int64_t)t * kKT * a.v_stride, a.v_stride, rows, vb, wave);
+    };
+
+    issue(kbuf0, vbuf0, 0);
+
+    // the wave's queries as B operands: row c of each block, values 16 s + 8 h ..
+    bf16x8 qf[QB][D / 16];
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+        const int r = wrow + qb * 32 + c;
+        load_row_operand<D>(qf[qb], a.q + (st.start + r) * a.q_stride + (int64_t)head * D, h, r < st.len);
+    }
+    const LaneOffsets<D> lo(lane);
+    const float cs = a.scale * kLog2e;           // exp(scale s) = exp2(cs s)
+    float m[QB], l[QB];
+    f32x16 o[QB][D / 32];
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+        m[qb] = kNegInf;
+        l[qb] = 0.f;
+#pragma unroll
+        for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[qb][db][i] = 0.f;
+    }
+
+    auto tile = [&](const uint8_t* kb, const uint8_t* vb, int t) {
+        f32x16 s[QB][2];
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb)
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) s[qb][n][i] = 0.f;
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int ds = 0; ds < D / 16; ++ds) {
+                const bf16x8 kf = lds_row(kb + n * 32 * T::kRowB, lo.row[ds]);
+#pragma unroll
+                for (int qb = 0; qb < QB; ++qb) s[qb][n] = mfma32(kf, qf[qb][ds], s[qb][n]);
+            }
+        if (t * kKT + kKT - 1 > wrow) {          // the tile reaches past the wave's first row
+#pragma unroll
+            for (int qb = 0; qb < QB; ++qb) {
+                const int r = wrow + qb * 32 + c - t * kKT - 4 * h;
+#pragma unroll
+                for (int n = 0; n < 2; ++n)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (n * 32 + (i & 3) + 8 * (i >> 2) > r) s[qb][n][i] = kNegInf;
+            }
+        }
+#pragma unroll
+        for (int qb = 0; qb < QB; ++qb) {
+            float mx = s[qb][0][0];
+#pragma unroll
+            for (int i = 1; i < 32; ++i) mx = fmaxf(mx, s[qb][i >> 4][i & 15]);
+            const float mn = fmaxf(m[qb], max_halves(mx) * cs);
+            if (__any(mn > m[qb])) {
+                const float alpha = exp2_fast(m[qb] - mn);
+                l[qb] *= alpha;
+#pragma unroll
+                for (int db = 0; db < D / 32; ++db)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[qb][db][i] *= alpha;
+                m[qb] = mn;
+            }
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float p = exp2_fast(__builtin_fmaf(s[qb][i >> 4][i & 15], cs, -m[qb]));
+                s[qb][i >> 4][i & 15] = p;
+                sum += p;
+            }
+            l[qb] += sum;
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n)
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8 p[QB];
+#pragma unroll
+                for (int qb = 0; qb < QB; ++qb) p[qb] = to_operand(s[qb][n], ks);
+#pragma unroll
+                for (int db = 0; db < D / 32; ++db) {
+                    const bf16x8 vf = lds_transposed(vb + (n * 32 + ks * 16) * T::kRowB, lo.tr[0][db], lo.tr[1][db]);
+#pragma unroll
+                    for (int qb = 0; qb < QB; ++qb) o[qb][db] = mfma32(vf, p[qb], o[qb][db]);
+                }
+            }
+    };
+
+    const int last = min(wrow + 32 * QB, st.len) - 1;    // the wave's last row
+    auto step = [&](const uint8_t* kb, const uint8_t* vb, uint8_t* knext, uint8_t* vnext, int t) {
+        wait_vm<0>();
+        stage_barrier();
+        if (t + 1 < tiles) issue(knext, vnext, t + 1);
+        if (t * kKT <= last && wrow < st.len) tile(kb, vb, t);
+    };
+    for (int t = 0; t < tiles; t += 2) {
+        step(kbuf0, vbuf0, kbuf1, vbuf1, t);
+        if (t + 1 < tiles) step(kbuf1, vbuf1, kbuf0, vbuf0, t + 1);
+    }
+
+#pragma unroll
+    for (int qb = 0; qb < QB; ++qb) {
+        const int r = wrow + qb * 32 + c;
+        const float sum = sum_halves(l[qb]);
+        store_transposed<D>(a.out + (st.start + r) * a.out_stride + (int64_t)head * D, o[qb], 1.f / sum, h, r < st.len);
+        if (a.lse != nullptr && h == 0 && r < st.len)
+            a.lse[(int64_t)head * a.total_T + st.start + r] = (m[qb] + __builtin_amdgcn_logf(sum)) * kLn2;
+    }
+}
+
+template <int D, int QB, int W>
+static hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
+    const int64_t blocks = (a.total_T / (32 * QB * W) + a.N) * a.Hq;
+    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((attn_fwd_kernel<D, QB, W>), dim3((uint32_t)blocks), dim3(64 * W), 0, s, a);
+    return hipGetLastError();
+}
+
+hipError_t launch_attn_prefill(const AttnArgs& a, int D, hipStream_t s) {
+    return D == 64 ? launch_fwd<64, 1, 4>(a, s) : launch_fwd<128, 1, 4>(a, s);
+}
+
+}  // namespace lfm2sc

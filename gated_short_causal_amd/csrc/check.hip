@@ -10,11 +10,13 @@
 #include <mutex>
 
 #include "common.hpp"
+#include "hybrid.hpp"
 #include "kernels.hpp"
 
 namespace lfm2sc {
 
 __device__ int g_check_flags;
+static std::mutex g_check_mutex;
 
 __global__ void check_reset_kernel() {
     if (threadIdx.x == 0) g_check_flags = 0;
@@ -46,10 +48,33 @@ __global__ void check_accept_kernel(const int32_t* __restrict__ acc, int N, int 
     if (acc[i] < 0 || acc[i] > L) atomicOr(&g_check_flags, (int)kBadAccept);
 }
 
+__global__ void check_range_kernel(const int32_t* __restrict__ v, int64_t n, int64_t lo, int64_t hi, int flag) {
+    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (i < n && (v[i] < lo || v[i] > hi)) atomicOr(&g_check_flags, flag);
+}
+
+// The arrays' entries that leave their ranges, as bits 0, 1, .. by array.
+int check_device_ranges(hipStream_t s, const RangeCheck* checks, int count, hipError_t* err) {
+    std::lock_guard<std::mutex> lock(g_check_mutex);
+    hipLaunchKernelGGL(check_reset_kernel, dim3(1), dim3(64), 0, s);
+    for (int k = 0; k < count; ++k) {
+        const RangeCheck& c = checks[k];
+        if (c.v != nullptr && c.n > 0)
+            hipLaunchKernelGGL(check_range_kernel, dim3((uint32_t)((c.n + 255) / 256)), dim3(256), 0, s, c.v, c.n, c.lo,
+                               c.hi, 1 << k);
+    }
+    int flags = 0;
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess) e = hipMemcpyFromSymbolAsync(&flags, HIP_SYMBOL(g_check_flags), sizeof(int), 0,
+                                                      hipMemcpyDeviceToHost, s);
+    if (e == hipSuccess) e = hipStreamSynchronize(s);
+    *err = e;
+    return flags;
+}
+
 int check_device_preconditions(hipStream_t s, const int32_t* slot_idx, int N, int64_t num_slots,
                                const int32_t* cu, int64_t total_T, const int32_t* accept, int L, hipError_t* err) {
-    static std::mutex mu;
-    std::lock_guard<std::mutex> lock(mu);
+    std::lock_guard<std::mutex> lock(g_check_mutex);
     *err = hipSuccess;
     const int tb = 256;
     hipLaunchKernelGGL(check_reset_kernel, dim3(1), dim3(64), 0, s);
