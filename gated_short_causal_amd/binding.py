@@ -116,7 +116,8 @@ def _dense(t, name, numel: int, dtype=None):
 
 
 def _stream(device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    # the raw handle, without the Stream object around it (1 us less per call)
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _hk(weight: torch.Tensor):

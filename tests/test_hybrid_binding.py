@@ -50,7 +50,7 @@ def test_prefill_marshals(lib):
     (dict(k=torch.zeros(10, 128)), TypeError), (dict(out=torch.zeros(10, 200, dtype=BF)), ValueError),
     (dict(out=torch.zeros(9, 256, dtype=BF)), ValueError), (dict(out=torch.zeros(10, 512, dtype=BF)), ValueError),
     (dict(cu_seqlens=torch.zeros(3, dtype=torch.int64)), TypeError), (dict(cu_seqlens=None), ValueError),
-    (dict(lse=torch.zeros(3, 10)), ValueError), (dict(lse=torch.zeros(4, 10, dtype=BF)), ValueError),
+    (dict(lse=torch.zeros(3, 10)), ValueError), (dict(lse=torch.zeros(4, 10, dtype=BF)), TypeError),
     (dict(q=torch.zeros(10, 512, dtype=BF)[:, ::2]), ValueError), (dict(D=0), ValueError),
 ])
 def test_prefill_refuses(lib, change, err):
@@ -138,7 +138,7 @@ def test_drafts_marshal(lib):
     (dict(target_probs=torch.zeros(8, 11)), ValueError), (dict(draft_probs=torch.zeros(6, 10)), ValueError),
     (dict(draft_probs=torch.zeros(6, 11, dtype=BF)), TypeError), (dict(draft_tokens=torch.zeros(6, dtype=I32)), ValueError),
     (dict(draft_tokens=torch.zeros(3, 2)), TypeError), (dict(u_accept=torch.zeros(5)), ValueError),
-    (dict(u_sample=torch.zeros(3, dtype=torch.float64)), ValueError), (dict(accept_len=torch.zeros(2, dtype=I32)), ValueError),
+    (dict(u_sample=torch.zeros(3, dtype=torch.float64)), TypeError), (dict(accept_len=torch.zeros(2, dtype=I32)), ValueError),
     (dict(next_token=torch.zeros(3)), TypeError), (dict(keep_len=torch.zeros(3)), TypeError),
     (dict(num_drafts=torch.zeros(1, dtype=I32)), ValueError), (dict(target_probs=torch.zeros(9, 11, dtype=torch.float16)), TypeError),
 ])
