@@ -143,7 +143,9 @@ size_t lfm2sc_attn_backward_workspace_bytes(int dtype, int D, int num_heads, int
     if (dtype != LFM2SC_BF16 || (D != 64 && D != 128) || num_kv_heads < 1 || num_heads < num_kv_heads ||
         num_heads % num_kv_heads != 0 || num_heads > kMaxHeads || total_T <= 0 || total_T >= kMaxRows || num_seqs <= 0)
         return 0;
-    return 2 * round_up((size_t)num_heads * (size_t)total_T * 4);
+    const size_t rows = 2 * round_up((size_t)num_heads * (size_t)total_T * 4);
+    const int splits = attn_backward_splits(num_heads, num_kv_heads, total_T, num_seqs);
+    return rows + (splits > 1 ? (size_t)splits * 2 * (size_t)total_T * (size_t)num_kv_heads * (size_t)D * 4 : 0);
 }
 
 int lfm2sc_attn_backward(int dtype, int D, int num_heads, int num_kv_heads, const void* q, int64_t q_stride, const void* k,
@@ -193,7 +195,10 @@ int lfm2sc_attn_backward(int dtype, int D, int num_heads, int num_kv_heads, cons
     a.dk = static_cast<uint16_t*>(dk); a.dk_stride = dk_stride;
     a.dv = static_cast<uint16_t*>(dv); a.dv_stride = dv_stride;
     a.delta = static_cast<float*>(workspace);
-    a.lse2 = reinterpret_cast<float*>(static_cast<char*>(workspace) + need / 2);
+    const size_t rows = round_up((size_t)num_heads * (size_t)total_T * 4);
+    a.lse2 = reinterpret_cast<float*>(static_cast<char*>(workspace) + rows);
+    a.splits = attn_backward_splits(num_heads, num_kv_heads, total_T, num_seqs);
+    a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 2 * rows);
     return launched(fn, launch_attn_backward(a, D, s));
 }
 

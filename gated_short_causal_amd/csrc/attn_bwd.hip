@@ -47,27 +47,29 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnGradArgs a) {
     }
 }
 
-// dk and dv: a wave owns 32 keys, a workgroup 32 W consecutive ones.  Two
-// stages of query tiles (q rows, dout rows) and their lse and delta in LDS.
-template <int D, int W>
-__device__ __forceinline__ void dkv_part(const AttnGradArgs& a, uint8_t* qb0, uint8_t* db0, uint8_t* qb1, uint8_t* db1,
-                                         float* lb0, float* eb0, float* lb1, float* eb1, int block, int wave, int lane) {
+// dk (kK) and dv (kV), or one of them: a wave owns 32 keys, a workgroup 32 W
+// consecutive ones, for G / splits query heads of the group.  Two stages of
+// query tiles (q rows, dout rows) and their lse and delta in LDS.
+template <int D, int W, bool kV, bool kK>
+__device__ __forceinline__ void kv_part(const AttnGradArgs& a, uint8_t* qb0, uint8_t* db0, uint8_t* qb1, uint8_t* db1,
+                                        float* lb0, float* eb0, float* lb1, float* eb1, int block, int wave, int lane) {
     using T = Tile<D>;
     constexpr int kBN = 32 * W;
     const int c = lane & 31, h = lane >> 5;
     const AttnArgs& f = a.f;
-    const int G = f.Hq / f.Hkv;
-    const int kvh = block % f.Hkv;
-    const SeqTile st = find_seq_tile<false>(f.cu, f.N, f.total_T, block / f.Hkv, kBN);
+    const int G = f.Hq / f.Hkv / a.splits;       // heads of this workgroup
+    const int kvh = block % f.Hkv, split = block / f.Hkv % a.splits;
+    const int head0 = (kvh * a.splits + split) * G;
+    const SeqTile st = find_seq_tile(f.cu, f.N, f.total_T, block / (f.Hkv * a.splits), kBN);
     if (st.len == 0) return;
-    const int n0 = st.block * kBN;
+    const int n0 = ((st.len + kBN - 1) / kBN - st.rank) * kBN;
     const int wkey = n0 + wave * 32;
     const int first = n0 / 64, last = (st.len + 63) / 64;     // query tiles [first, last) of 64 rows
     const int per_head = last - first, steps = per_head * G;
 
     const TileCopy<D, W> qcopy(wave, lane, f.q_stride), dcopy(wave, lane, a.dout_stride);
     auto issue = [&](uint8_t* qb, uint8_t* db, float* lb, float* eb, int step) {
-        const int head = kvh * G + step / per_head, t = first + step % per_head;
+        const int head = head0 + step / per_head, t = first + step % per_head;
         const int rows = min(64, st.len - t * 64);
         const int64_t row = st.start + (int64_t)t * 64;
         qcopy(f.q + row * f.q_stride + (int64_t)head * D, f.q_stride, rows, qb, wave);
@@ -75,7 +77,8 @@ __device__ __forceinline__ void dkv_part(const AttnGradArgs& a, uint8_t* qb0, ui
         if (wave == 0) {
             const int64_t at = (int64_t)head * f.total_T + row;
             __builtin_amdgcn_raw_ptr_buffer_load_lds(row_rsrc(a.lse2 + at, rows * 4), (lds_ptr_t)lb, 4, lane * 4, 0, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_rsrc(a.delta + at, rows * 4), (lds_ptr_t)eb, 4, lane * 4, 0, 0, 0);
+            if constexpr (kK)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(row_rsrc(a.delta + at, rows * 4), (lds_ptr_t)eb, 4, lane * 4, 0, 0, 0);
         }
     };
     issue(qb0, db0, lb0, eb0, 0);
@@ -84,7 +87,7 @@ __device__ __forceinline__ void dkv_part(const AttnGradArgs& a, uint8_t* qb0, ui
     const bool exists = wkey + c < st.len;
     const int64_t krow = st.start + wkey + c;
     load_row_operand<D>(kf, f.k + krow * f.k_stride + (int64_t)kvh * D, h, exists);
-    load_row_operand<D>(vf, f.v + krow * f.v_stride + (int64_t)kvh * D, h, exists);
+    if constexpr (kK) load_row_operand<D>(vf, f.v + krow * f.v_stride + (int64_t)kvh * D, h, exists);
     const LaneOffsets<D> lo(lane);
     const float cs = f.scale * kLog2e;
     f32x16 dk[D / 32], dv[D / 32];
@@ -93,48 +96,61 @@ __device__ __forceinline__ void dkv_part(const AttnGradArgs& a, uint8_t* qb0, ui
 #pragma unroll
         for (int i = 0; i < 16; ++i) dk[b][i] = dv[b][i] = 0.f;
 
-    auto tile = [&](const uint8_t* qb, const uint8_t* db, const float* lb, const float* eb, int t) {
+    // 32 query rows (n * 32 .. of the tile) against the wave's keys
+    auto rows32 = [&](const uint8_t* qb, const uint8_t* db, const float* lb, const float* eb, int n, int r0) {
+        f32x16 s, e;
+        bf16x8 p[2], g[2];
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {            // 32 query rows at a time
-            const int r0 = t * 64 + n * 32;
-            if (r0 + 31 < wkey) continue;        // all before the wave's keys
-            f32x16 s, e;
+        for (int i = 0; i < 16; ++i) s[i] = e[i] = 0.f;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = e[i] = 0.f;
+        for (int ds = 0; ds < D / 16; ++ds) s = mfma32(lds_row(qb + n * 32 * T::kRowB, lo.row[ds]), kf[ds], s);
+        if constexpr (kK) {
 #pragma unroll
-            for (int ds = 0; ds < D / 16; ++ds) {
-                s = mfma32(lds_row(qb + n * 32 * T::kRowB, lo.row[ds]), kf[ds], s);
-                e = mfma32(lds_row(db + n * 32 * T::kRowB, lo.row[ds]), vf[ds], e);
-            }
-            f32x16 lse, del;
+            for (int ds = 0; ds < D / 16; ++ds) e = mfma32(lds_row(db + n * 32 * T::kRowB, lo.row[ds]), vf[ds], e);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 x = *reinterpret_cast<const float4*>(lb + n * 32 + 8 * j + 4 * h);
+            s[4 * j] = exp2_fast(__builtin_fmaf(s[4 * j], cs, -x.x));
+            s[4 * j + 1] = exp2_fast(__builtin_fmaf(s[4 * j + 1], cs, -x.y));
+            s[4 * j + 2] = exp2_fast(__builtin_fmaf(s[4 * j + 2], cs, -x.z));
+            s[4 * j + 3] = exp2_fast(__builtin_fmaf(s[4 * j + 3], cs, -x.w));
+        }
+        if (r0 < wkey + 31) {                    // the first of the rows lies before the wave's last key
+            const int key = wkey + c - r0 - 4 * h;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                if ((i & 3) + 8 * (i >> 2) < key) s[i] = 0.f;
+        }
+        if constexpr (kV) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) p[ks] = to_operand(s, ks);
+        }
+        if constexpr (kK) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float4 x = *reinterpret_cast<const float4*>(lb + n * 32 + 8 * j + 4 * h);
                 const float4 y = *reinterpret_cast<const float4*>(eb + n * 32 + 8 * j + 4 * h);
-                lse[4 * j] = x.x; lse[4 * j + 1] = x.y; lse[4 * j + 2] = x.z; lse[4 * j + 3] = x.w;
-                del[4 * j] = y.x; del[4 * j + 1] = y.y; del[4 * j + 2] = y.z; del[4 * j + 3] = y.w;
+                e[4 * j] = s[4 * j] * (e[4 * j] - y.x);
+                e[4 * j + 1] = s[4 * j + 1] * (e[4 * j + 1] - y.y);
+                e[4 * j + 2] = s[4 * j + 2] * (e[4 * j + 2] - y.z);
+                e[4 * j + 3] = s[4 * j + 3] * (e[4 * j + 3] - y.w);
             }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[i] = exp2_fast(__builtin_fmaf(s[i], cs, -lse[i]));
-            if (r0 < wkey + 31) {
-                const int key = wkey + c - r0 - 4 * h;
+            for (int ks = 0; ks < 2; ++ks) g[ks] = to_operand(e, ks);
+        }
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    if ((i & 3) + 8 * (i >> 2) < key) s[i] = 0.f;
-            }
+        for (int ks = 0; ks < 2; ++ks) {
+            const int at = (n * 32 + ks * 16) * T::kRowB;
 #pragma unroll
-            for (int i = 0; i < 16; ++i) e[i] = s[i] * (e[i] - del[i]);
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const bf16x8 p = to_operand(s, ks), g = to_operand(e, ks);
-                const int at = (n * 32 + ks * 16) * T::kRowB;
-#pragma unroll
-                for (int b = 0; b < D / 32; ++b) {
-                    dv[b] = mfma32(lds_transposed(db + at, lo.tr[0][b], lo.tr[1][b]), p, dv[b]);
-                    dk[b] = mfma32(lds_transposed(qb + at, lo.tr[0][b], lo.tr[1][b]), g, dk[b]);
-                }
+            for (int b = 0; b < D / 32; ++b) {
+                if constexpr (kV) dv[b] = mfma32(lds_transposed(db + at, lo.tr[0][b], lo.tr[1][b]), p[ks], dv[b]);
+                if constexpr (kK) dk[b] = mfma32(lds_transposed(qb + at, lo.tr[0][b], lo.tr[1][b]), g[ks], dk[b]);
             }
         }
+    };
+    auto tile = [&](const uint8_t* qb, const uint8_t* db, const float* lb, const float* eb, int t) {
+        if (t * 64 + 31 >= wkey) rows32(qb, db, lb, eb, 0, t * 64);
+        if (t * 64 + 63 >= wkey) rows32(qb, db, lb, eb, 1, t * 64 + 32);
     };
     auto step = [&](const uint8_t* qb, const uint8_t* db, const float* lb, const float* eb, uint8_t* qn, uint8_t* dn,
                     float* ln, float* en, int i) {
@@ -147,8 +163,50 @@ __device__ __forceinline__ void dkv_part(const AttnGradArgs& a, uint8_t* qb0, ui
         step(qb0, db0, lb0, eb0, qb1, db1, lb1, eb1, i);
         if (i + 1 < steps) step(qb1, db1, lb1, eb1, qb0, db0, lb0, eb0, i + 1);
     }
-    store_transposed<D>(a.dk + krow * a.dk_stride + (int64_t)kvh * D, dk, f.scale, h, exists);
-    store_transposed<D>(a.dv + krow * a.dv_stride + (int64_t)kvh * D, dv, 1.f, h, exists);
+    if (a.splits == 1) {
+        if constexpr (kK) store_transposed<D>(a.dk + krow * a.dk_stride + (int64_t)kvh * D, dk, f.scale, h, exists);
+        if constexpr (kV) store_transposed<D>(a.dv + krow * a.dv_stride + (int64_t)kvh * D, dv, 1.f, h, exists);
+    } else if (exists) {
+        const int64_t one = f.total_T * f.Hkv * D;           // [split][dk, dv][total_T][Hkv * D] fp32
+        float* p = a.part + 2 * split * one + (krow * f.Hkv + kvh) * D + 4 * h;
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+                float* x = p + 32 * b + 2 * i;
+                if constexpr (kK)
+                    *reinterpret_cast<float4*>(x) = make_float4(dk[b][i], dk[b][i + 1], dk[b][i + 2], dk[b][i + 3]);
+                if constexpr (kV)
+                    *reinterpret_cast<float4*>(x + one) = make_float4(dv[b][i], dv[b][i + 1], dv[b][i + 2], dv[b][i + 3]);
+            }
+    }
+}
+
+// Adds up the splits of dk and dv: a workgroup takes 32 rows of a sequence.
+template <int D>
+__global__ __launch_bounds__(256) void attn_dkv_sum_kernel(AttnGradArgs a) {
+    const AttnArgs& f = a.f;
+    const SeqTile st = find_seq_tile(f.cu, f.N, f.total_T, blockIdx.x, 32);
+    if (st.len == 0) return;
+    const int row0 = (st.rank - 1) * 32, rows = min(32, st.len - row0);
+    const int per_row = f.Hkv * D / 4;
+    const int64_t one = f.total_T * f.Hkv * D;
+    for (int i = threadIdx.x; i < rows * per_row; i += 256) {
+        const int64_t row = st.start + row0 + i / per_row;
+        const int col = i % per_row * 4;
+        const float* p = a.part + row * f.Hkv * D + col;
+        float4 k = *reinterpret_cast<const float4*>(p), v = *reinterpret_cast<const float4*>(p + one);
+        for (int s = 1; s < a.splits; ++s) {
+            const float4 x = *reinterpret_cast<const float4*>(p + 2 * s * one);
+            const float4 y = *reinterpret_cast<const float4*>(p + (2 * s + 1) * one);
+            k.x += x.x; k.y += x.y; k.z += x.z; k.w += x.w;
+            v.x += y.x; v.y += y.y; v.z += y.z; v.w += y.w;
+        }
+        *reinterpret_cast<uint2*>(a.dk + row * a.dk_stride + col) =
+            make_uint2(Elem<uint16_t>::pack2(k.x * f.scale, k.y * f.scale), Elem<uint16_t>::pack2(k.z * f.scale, k.w * f.scale));
+        *reinterpret_cast<uint2*>(a.dv + row * a.dv_stride + col) =
+            make_uint2(Elem<uint16_t>::pack2(v.x, v.y), Elem<uint16_t>::pack2(v.z, v.w));
+    }
 }
 
 // dq: a wave owns 32 query rows of one head, a workgroup 32 W consecutive ones.
@@ -161,9 +219,9 @@ __device__ __forceinline__ void dq_part(const AttnGradArgs& a, uint8_t* kb0, uin
     const AttnArgs& f = a.f;
     const int G = f.Hq / f.Hkv;
     const int kvh = block % f.Hkv, head = kvh * G + (block / f.Hkv) % G;
-    const SeqTile st = find_seq_tile<true>(f.cu, f.N, f.total_T, block / f.Hq, kBM);
+    const SeqTile st = find_seq_tile(f.cu, f.N, f.total_T, block / f.Hq, kBM);
     if (st.len == 0) return;
-    const int q0 = st.block * kBM;
+    const int q0 = (st.rank - 1) * kBM;
     const int wrow = q0 + wave * 32;
     const int tiles = (min(q0 + kBM, st.len) + 63) / 64;
 
@@ -240,35 +298,62 @@ __device__ __forceinline__ void dq_part(const AttnGradArgs& a, uint8_t* kb0, uin
     store_transposed<D>(a.dq + row * a.dq_stride + (int64_t)head * D, dq, f.scale, h, exists);
 }
 
-// Both kinds of workgroup in one launch, the key blocks first: they run
-// longest (a group's heads one after the other), and the query blocks fill in
-// behind them.
-template <int D, int W>
-__global__ __launch_bounds__(64 * W, D == 64 ? 2 : 1) void attn_grad_kernel(AttnGradArgs a, int dkv_blocks) {
+// All kinds of workgroup in one launch, the key blocks first: they run longest,
+// and the query blocks fill in behind them.  kApart: dk and dv in workgroups of
+// their own: for D = 128 the accumulators of both leave one wave per SIMD (341
+// registers), and forming p once more for dv costs less than losing the second
+// wave (13 packed sequences of up to 1531 rows, 16 heads of 128: 216 -> 192 us;
+// for D = 64 both fit, and apart they take 1030 instead of 907 us at T = 8192).
+template <int D, int W, bool kApart>
+__global__ __launch_bounds__(64 * W, 2) void attn_grad_kernel(AttnGradArgs a, int kv_blocks) {
     constexpr int kTileB = 64 * Tile<D>::kRowB;
     __shared__ __attribute__((aligned(1024))) uint8_t x0[kTileB], y0[kTileB], x1[kTileB], y1[kTileB];
     __shared__ __attribute__((aligned(1024))) float l0[64], e0[64], l1[64], e1[64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    if ((int)blockIdx.x < dkv_blocks) dkv_part<D, W>(a, x0, y0, x1, y1, l0, e0, l1, e1, blockIdx.x, wave, lane);
-    else dq_part<D, W>(a, x0, y0, x1, y1, blockIdx.x - dkv_blocks, wave, lane);
+    const int b = blockIdx.x;
+    if (b < kv_blocks) {
+        kv_part<D, W, !kApart, true>(a, x0, y0, x1, y1, l0, e0, l1, e1, b, wave, lane);
+    } else if (kApart && b < 2 * kv_blocks) {
+        kv_part<D, W, true, false>(a, x0, y0, x1, y1, l0, e0, l1, e1, b - kv_blocks, wave, lane);
+    } else {
+        dq_part<D, W>(a, x0, y0, x1, y1, b - (kApart ? 2 : 1) * kv_blocks, wave, lane);
+    }
 }
 
-template <int D, int W>
+constexpr int kGW = 4;                           // waves per workgroup
+
+// Workgroups that share the query heads of a key block.  A key block's
+// workgroup walks its group's heads one after the other; with fewer than two of
+// them per CU the first key blocks' walks outlast everything else, so the heads
+// are dealt to several workgroups whose fp32 sums are added up afterwards
+// (T = 4096, 32 / 8 heads of 64: 1 -> 363 us, 2 -> 253 + 10 us, 4 -> 257 + 19 us;
+// T = 8192, 512 workgroups already: 1 -> 917 us, 2 -> 922 + 14 us).
+int attn_backward_splits(int Hq, int Hkv, int64_t total_T, int N) {
+    const int G = Hq / Hkv;
+    const int64_t blocks = (total_T / (32 * kGW) + 1) * Hkv;
+    for (int s = 1; s < G; ++s)
+        if (G % s == 0 && blocks * s >= 512) return s;
+    return G;
+}
+
+template <int D, bool kApart>
 static hipError_t launch_bwd(const AttnGradArgs& a, hipStream_t s) {
     const AttnArgs& f = a.f;
-    const int64_t per_row = f.total_T / (32 * W) + f.N;
-    if (per_row * (f.Hkv + f.Hq) >= ((int64_t)1 << 31) || f.total_T / 32 >= ((int64_t)1 << 31) - 1) return hipErrorInvalidConfiguration;
+    const int64_t rows = 32 * kGW, per_row = f.N == 1 ? (f.total_T + rows - 1) / rows : f.total_T / rows + f.N;
+    const int64_t kv = per_row * f.Hkv * a.splits, all = kv * (kApart ? 2 : 1) + per_row * f.Hq;
+    const int64_t sums = f.total_T / 32 + f.N;
+    if (all >= ((int64_t)1 << 31) || sums >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
     const int heads = 64 / (D / 8);
     hipLaunchKernelGGL((attn_delta_kernel<D>), dim3((uint32_t)((f.total_T + 31) / 32), (f.Hq + heads - 1) / heads), dim3(256),
                        0, s, a);
-    hipLaunchKernelGGL((attn_grad_kernel<D, W>), dim3((uint32_t)(per_row * (f.Hkv + f.Hq))), dim3(64 * W), 0, s, a,
-                       (int)(per_row * f.Hkv));
+    hipLaunchKernelGGL((attn_grad_kernel<D, kGW, kApart>), dim3((uint32_t)all), dim3(64 * kGW), 0, s, a, (int)kv);
+    if (a.splits > 1) hipLaunchKernelGGL((attn_dkv_sum_kernel<D>), dim3((uint32_t)sums), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
 hipError_t launch_attn_backward(const AttnGradArgs& a, int D, hipStream_t s) {
-    return D == 64 ? launch_bwd<64, 4>(a, s) : launch_bwd<128, 4>(a, s);
+    return D == 64 ? launch_bwd<64, false>(a, s) : launch_bwd<128, true>(a, s);
 }
 
 }  // namespace lfm2sc

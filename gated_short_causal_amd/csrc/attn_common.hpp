@@ -106,13 +106,14 @@ __device__ __forceinline__ bf16x8 lds_transposed(const uint8_t* tile, uint32_t o
     return __builtin_bit_cast(bf16x8, r);
 }
 
-// Copies of 64-row tiles (row r at byte (r * stride) * 2 from the tile's first
+// Copies of R-row tiles (row r at byte (r * stride) * 2 from the tile's first
 // row) to LDS, kDma KiB per wave; rows at or beyond the given count read as
 // zeros (the buffer's range check).
-template <int D, int W>
+template <int D, int W, int R = 64>
 struct TileCopy {
     using T = Tile<D>;
-    static constexpr int kDma = 64 * T::kRowB / 1024 / W;
+    static constexpr int kDma = R * T::kRowB / 1024 / W;
+    static_assert(kDma * W * 1024 == R * T::kRowB, "whole copies");
     uint32_t off[kDma];
     __device__ TileCopy(int wave, int lane, int64_t stride) {
 #pragma unroll
@@ -162,51 +163,85 @@ __device__ __forceinline__ void store_transposed(uint16_t* row, const f32x16 (&x
         }
 }
 
-// Sequence and row block of the tile-th block of `rows` rows, over the
-// sequences in order; within a sequence from its end to its start (kFromEnd:
-// the causal query blocks with most keys are handed out first) or from its
-// start (the key blocks that most queries see).  Row offsets are clamped to
+// Sum over the wave, the same in every lane (DPP row shifts, then row broadcasts).
+__device__ __forceinline__ int wave_sum(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);    // row_shr:1
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);    // row_shr:2
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);    // row_shr:4
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);    // row_shr:8
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);    // row_bcast:15
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);    // row_bcast:31
+    return __builtin_amdgcn_readlane(x, 63);
+}
+
+// Row blocks of packed sequences in order of falling work.  A sequence of len
+// rows has nb = ceil(len / rows) blocks; rank r = 1 .. nb counts them from the
+// end that costs least (forward: rank = block + 1, the keys it sees; key blocks
+// of the backward: rank = nb - block, the queries that see it).  The tile-th
+// block overall is found from F(r) = sum_i max(0, nb_i - r), the number of
+// blocks of a rank above r: a binary search over r, all lanes of the wave
+// summing over the sequences, 64 at a time.  Row offsets are clamped to
 // [0, total_T].  len == 0: no such block.  Wave-uniform.
+//
+// Handing out the heaviest blocks first, whatever their sequence, keeps a long
+// sequence at the end of the batch from running on alone.
 struct SeqTile {
     int64_t start;    // first packed row of the sequence
     int len;          // its length
-    int block;        // row block within it
+    int rank;         // 1 .. ceil(len / rows)
 };
-template <bool kFromEnd>
+struct SeqRange {
+    int start, len;
+};
+__device__ __forceinline__ SeqRange seq_range(const int32_t* __restrict__ cu, int s, int N, int64_t total_T) {
+    if (s >= N) return SeqRange{0, 0};
+    const int64_t lo = min(max((int64_t)cu[s], (int64_t)0), total_T);
+    const int64_t hi = min(max((int64_t)cu[s + 1], (int64_t)0), total_T);
+    return SeqRange{(int)lo, hi > lo ? (int)(hi - lo) : 0};
+}
 __device__ __forceinline__ SeqTile find_seq_tile(const int32_t* __restrict__ cu, int N, int64_t total_T, int tile,
                                                  int rows) {
     const int lane = threadIdx.x & 63;
-    int base = 0;
+    const SeqRange own = seq_range(cu, lane, N, total_T);        // sequences 0 .. 63
+    const int nb = (own.len + rows - 1) / rows;
+    if (N == 1) {
+        const int all = __builtin_amdgcn_readfirstlane(nb);
+        if (tile >= all) return SeqTile{0, 0, 0};
+        return SeqTile{__builtin_amdgcn_readfirstlane(own.start), __builtin_amdgcn_readfirstlane(own.len), all - tile};
+    }
+    auto above = [&](int r) {
+        int n = max(nb - r, 0);
+        for (int s = 64 + lane; s < N; s += 64) n += max((seq_range(cu, s, N, total_T).len + rows - 1) / rows - r, 0);
+        return wave_sum(n);
+    };
+    if (tile >= above(0)) return SeqTile{0, 0, 0};
+    int lo = 0, hi = 1;                          // F(lo) > tile >= F(hi)
+    int at = above(1);
+    while (at > tile) {
+        lo = hi;
+        hi *= 2;
+        at = above(hi);
+    }
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1, f = above(mid);
+        if (f > tile) lo = mid;
+        else {
+            hi = mid;
+            at = f;
+        }
+    }
+    int left = tile - at;                        // which of the sequences with a block of rank hi
     for (int s0 = 0; s0 < N; s0 += 64) {
-        const int s = s0 + lane;
-        int a = 0, len = 0;
-        if (s < N) {
-            const int64_t lo = min(max((int64_t)cu[s], (int64_t)0), total_T);
-            const int64_t hi = min(max((int64_t)cu[s + 1], (int64_t)0), total_T);
-            a = (int)lo;
-            len = hi > lo ? (int)(hi - lo) : 0;
+        const SeqRange x = s0 == 0 ? own : seq_range(cu, s0 + lane, N, total_T);
+        const bool has = (x.len + rows - 1) / rows >= hi;
+        const uint64_t which = __ballot(has);
+        const int count = __popcll(which);
+        if (left < count) {
+            const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(which >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)which, 0));
+            const int l = __builtin_ctzll(__ballot(has && before == left));
+            return SeqTile{__builtin_amdgcn_readlane(x.start, l), __builtin_amdgcn_readlane(x.len, l), hi};
         }
-        const int n = (len + rows - 1) / rows;
-        int incl = n;
-        if (N > 1) {
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int up = __shfl_up(incl, d, 64);
-                if (lane >= d) incl += up;
-            }
-        } else {
-            incl = __builtin_amdgcn_readfirstlane(n);
-        }
-        const uint64_t hit = __ballot(tile < base + incl && n > 0 && tile >= base + incl - n);
-        if (hit != 0) {
-            const int l = __builtin_ctzll(hit);
-            SeqTile r;
-            r.start = __builtin_amdgcn_readlane(a, l);
-            r.len = __builtin_amdgcn_readlane(len, l);
-            r.block = __builtin_amdgcn_readlane(kFromEnd ? base + incl - 1 - tile : tile - (base + incl - n), l);
-            return r;
-        }
-        base += __builtin_amdgcn_readlane(incl, 63);
+        left -= count;
     }
     return SeqTile{0, 0, 0};
 }

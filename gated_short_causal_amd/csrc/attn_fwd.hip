@@ -13,12 +13,22 @@
 
 namespace lfm2sc {
 
-constexpr int kKT = 64;     // keys per staged tile
+constexpr float kLazy = 8.f;
 
-template <int D, int QB, int W>
-__global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a) {
+// A launch of one sequence whose workgroups are all resident at once: CU i gets
+// blocks i, i + 256, .. in falling order, so the CUs with the first of each
+// round would get all the heavy ones.  Every other round of `fold` row blocks
+// runs the other way (T = 4096, 32 heads of 64: 87 -> 82 us).
+__device__ __forceinline__ int folded(int t, int blocks, int fold) {
+    if (fold < 2) return t;
+    const int round = t / fold;
+    return (round & 1) && (round + 1) * fold <= blocks ? round * fold + fold - 1 - t % fold : t;
+}
+
+template <int D, int QB, int W, int kKT>
+__global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a, int fold) {
     using T = Tile<D>;
-    constexpr int kBM = 32 * QB * W;
+    constexpr int kBM = 32 * QB * W, NB = kKT / 32;
     constexpr int kTileB = kKT * T::kRowB;
     __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[kTileB], kbuf1[kTileB], vbuf0[kTileB], vbuf1[kTileB];
 
@@ -29,15 +39,15 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a) {
     const int G = a.Hq / a.Hkv;
     const int b = blockIdx.x;
     const int kvh = b % a.Hkv, head = kvh * G + (b / a.Hkv) % G;
-    const SeqTile st = find_seq_tile<true>(a.cu, a.N, a.total_T, b / a.Hq, kBM);
+    const SeqTile st = find_seq_tile(a.cu, a.N, a.total_T, folded(b / a.Hq, gridDim.x / a.Hq, fold), kBM);
     if (st.len == 0) return;
-    const int q0 = st.block * kBM;
+    const int q0 = (st.rank - 1) * kBM;
     const int wrow = q0 + wave * 32 * QB;        // the wave's first row in the sequence
     const int tiles = (min(q0 + kBM, st.len) + kKT - 1) / kKT;
 
     const uint16_t* kp = a.k + st.start * a.k_stride + (int64_t)kvh * D;
     const uint16_t* vp = a.v + st.start * a.v_stride + (int64_t)kvh * D;
-    const TileCopy<D, W> kcopy(wave, lane, a.k_stride), vcopy(wave, lane, a.v_stride);
+    const TileCopy<D, W, kKT> kcopy(wave, lane, a.k_stride), vcopy(wave, lane, a.v_stride);
     auto issue = [&](uint8_t* kb, uint8_t* vb, int t) {
         const int rows = min(kKT, st.len - t * kKT);
         kcopy(kp + (int64_t)t * kKT * a.k_stride, a.k_stride, rows, kb, wave);
@@ -68,15 +78,15 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a) {
     }
 
     auto tile = [&](const uint8_t* kb, const uint8_t* vb, int t) {
-        f32x16 s[QB][2];
+        f32x16 s[QB][NB];
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb)
 #pragma unroll
-            for (int n = 0; n < 2; ++n)
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) s[qb][n][i] = 0.f;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int ds = 0; ds < D / 16; ++ds) {
                 const bf16x8 kf = lds_row(kb + n * 32 * T::kRowB, lo.row[ds]);
@@ -88,7 +98,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a) {
             for (int qb = 0; qb < QB; ++qb) {
                 const int r = wrow + qb * 32 + c - t * kKT - 4 * h;
 #pragma unroll
-                for (int n = 0; n < 2; ++n)
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (n * 32 + (i & 3) + 8 * (i >> 2) > r) s[qb][n][i] = kNegInf;
@@ -98,20 +108,22 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a) {
         for (int qb = 0; qb < QB; ++qb) {
             float mx = s[qb][0][0];
 #pragma unroll
-            for (int i = 1; i < 32; ++i) mx = fmaxf(mx, s[qb][i >> 4][i & 15]);
-            const float mn = fmaxf(m[qb], max_halves(mx) * cs);
-            if (__any(mn > m[qb])) {
-                const float alpha = exp2_fast(m[qb] - mn);
+            for (int i = 1; i < 16 * NB; ++i) mx = fmaxf(mx, s[qb][i >> 4][i & 15]);
+            // m is a reference, not the maximum: it moves only when a row's maximum passes it by 2^kLazy, so most tiles
+            // rescale nothing.  p stays below 2^kLazy, whose bf16 and fp32 values are as exact as those below 1.
+            const float mn = max_halves(mx) * cs;
+            if (__any(mn > m[qb] + kLazy)) {
+                const float ref = fmaxf(m[qb], mn), alpha = exp2_fast(m[qb] - ref);
                 l[qb] *= alpha;
 #pragma unroll
                 for (int db = 0; db < D / 32; ++db)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) o[qb][db][i] *= alpha;
-                m[qb] = mn;
+                m[qb] = ref;
             }
             float sum = 0.f;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
+            for (int i = 0; i < 16 * NB; ++i) {
                 const float p = exp2_fast(__builtin_fmaf(s[qb][i >> 4][i & 15], cs, -m[qb]));
                 s[qb][i >> 4][i & 15] = p;
                 sum += p;
@@ -119,7 +131,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a) {
             l[qb] += sum;
         }
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
+        for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
                 bf16x8 p[QB];
@@ -156,16 +168,20 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a) {
     }
 }
 
-template <int D, int QB, int W>
+template <int D, int QB, int W, int KT>
 static hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
-    const int64_t blocks = (a.total_T / (32 * QB * W) + a.N) * a.Hq;
+    // sum ceil(len / rows) over the sequences is at most this
+    const int64_t rows = 32 * QB * W, per_head = a.N == 1 ? (a.total_T + rows - 1) / rows : a.total_T / rows + a.N;
+    const int64_t blocks = per_head * a.Hq;
     if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((attn_fwd_kernel<D, QB, W>), dim3((uint32_t)blocks), dim3(64 * W), 0, s, a);
+    constexpr int kResident = 256 * (D == 64 ? 4 : 3);           // workgroups
+    const int fold = a.N == 1 && blocks <= kResident ? 256 / a.Hq : 0;
+    hipLaunchKernelGGL((attn_fwd_kernel<D, QB, W, KT>), dim3((uint32_t)blocks), dim3(64 * W), 0, s, a, fold);
     return hipGetLastError();
 }
 
 hipError_t launch_attn_prefill(const AttnArgs& a, int D, hipStream_t s) {
-    return D == 64 ? launch_fwd<64, 1, 4>(a, s) : launch_fwd<128, 1, 4>(a, s);
+    return D == 64 ? launch_fwd<64, 1, 4, 64>(a, s) : launch_fwd<128, 1, 4, 32>(a, s);
 }
 
 }  // namespace lfm2sc

@@ -30,6 +30,8 @@ struct AttnGradArgs {
     uint16_t* dv; int64_t dv_stride;
     float* delta;                        // workspace, [Hq][total_T]
     float* lse2;                         // workspace, [Hq][total_T]
+    float* part;                         // workspace, [splits][2][total_T][Hkv * D] when splits > 1
+    int splits;                          // workgroups that share a key block's query heads
 };
 
 struct CachedArgs {
@@ -75,6 +77,7 @@ struct RangeCheck {
 int check_device_ranges(hipStream_t s, const RangeCheck* checks, int count, hipError_t* err);
 
 hipError_t launch_attn_prefill(const AttnArgs& a, int D, hipStream_t s);
+int attn_backward_splits(int Hq, int Hkv, int64_t total_T, int N);
 hipError_t launch_attn_backward(const AttnGradArgs& a, int D, hipStream_t s);
 hipError_t launch_attn_cached(CachedArgs a, int D, hipStream_t s);
 template <typename E>
