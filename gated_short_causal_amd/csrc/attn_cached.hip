@@ -15,15 +15,19 @@
 
 namespace lfm2sc {
 
-constexpr int kCW = 4;                        // waves per workgroup
+constexpr int kCW = 4;                        // waves per workgroup of the split form
 constexpr int kCRows = 32 * kCW;              // query rows of a prefix workgroup
 constexpr int kPrefixTile = 64;               // keys per staged tile, prefix
-template <int D> constexpr int kSuffixTile = 4096 / D;   // keys per wave's tile, suffix: 8 KiB of K, 8 KiB of V
+constexpr int kOwnTile = 32;                  // keys per wave's tile, suffix
+constexpr int kDirectW = 8;                   // waves per workgroup of the direct form
+constexpr float kLazy = 8.f;                  // as in attn_fwd.hip: how far (log2) a maximum may pass the reference
 
-// Row number in the pool of key idx of a page list; idx < 2^31.  A page number
-// outside the pool reads as the nearest page of it.
-__device__ __forceinline__ uint32_t pool_row(const CachedArgs& a, const int32_t* pages, int idx) {
-    const int p = min(max(pages[idx >> a.page_shift], 0), a.num_pages - 1);
+// Row number in the pool of key idx (< 2^31), whose page number is `page`.  A
+// page number outside the pool reads as the nearest page of it.  The number is
+// loaded a tile ahead and only looked at when it is used: clamping it at once
+// would wait for it, and with it for the copies issued before it.
+__device__ __forceinline__ uint32_t pool_row(const CachedArgs& a, int32_t page, int idx) {
+    const int p = min(max(page, 0), a.num_pages - 1);
     return ((uint32_t)p << a.page_shift) + (uint32_t)(idx & ((1 << a.page_shift) - 1));
 }
 
@@ -42,7 +46,8 @@ __device__ __forceinline__ void copy_paged(const uint16_t* pool, int64_t stride,
     }
 }
 
-// Running softmax state of a wave's 32 query rows (one per lane pair c, c + 32).
+// Running softmax state of a wave's 32 query rows (one per lane pair c, c + 32):
+// the reference m, sum l and output o, all relative to 2^m.
 template <int D>
 struct Rows {
     float m, l;
@@ -57,8 +62,9 @@ struct Rows {
     }
 };
 
-// One staged tile of KT keys against the wave's rows.  Keys numbered above
-// `seen` (the lane's row's last visible key within the tile) are masked.
+// One staged tile of KT keys against the wave's rows.  If `masked` (uniform),
+// keys numbered above `seen`, the lane's row's last visible key within the
+// tile, are masked.  A row that has seen no key keeps m = -inf and o = l = 0.
 template <int D, int KT>
 __device__ __forceinline__ void attend(Rows<D>& r, const bf16x8 (&qf)[D / 16], const uint8_t* kb, const uint8_t* vb,
                                        const LaneOffsets<D>& lo, float cs, bool masked, int seen, int h) {
@@ -83,22 +89,26 @@ __device__ __forceinline__ void attend(Rows<D>& r, const bf16x8 (&qf)[D / 16], c
     for (int n = 0; n < KT / 32; ++n)
 #pragma unroll
         for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[n][i]);
-    const float mn = fmaxf(r.m, max_halves(mx) * cs);
-    const float ref = mn == kNegInf ? 0.f : mn;      // a row that has seen no key yet: every p is 0
-    const float alpha = exp2_fast(r.m - ref);
-    r.m = mn;
-    r.l *= alpha;
+    const float mn = max_halves(mx) * cs;
+    if (__any(mn > r.m + kLazy)) {
+        const float m = fmaxf(r.m, mn), alpha = exp2_fast(r.m - (m == kNegInf ? 0.f : m));
+        r.m = m;
+        r.l *= alpha;
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
+        for (int b = 0; b < D / 32; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) r.o[b][i] *= alpha;
+            for (int i = 0; i < 16; ++i) r.o[b][i] *= alpha;
+    }
+    const float ref = r.m == kNegInf ? 0.f : r.m;
+    float sum = 0.f;
 #pragma unroll
     for (int n = 0; n < KT / 32; ++n)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             s[n][i] = exp2_fast(__builtin_fmaf(s[n][i], cs, -ref));
-            r.l += s[n][i];
+            sum += s[n][i];
         }
+    r.l += sum;
 #pragma unroll
     for (int n = 0; n < KT / 32; ++n)
 #pragma unroll
@@ -132,8 +142,10 @@ __device__ __forceinline__ void store_part(const CachedArgs& a, int split, const
     if (h == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(r.m, l);
 }
 
+// The prefix's keys [split] for 128 query rows of one head; the waves share the
+// staged tiles, two buffers of K and V.
 template <int D>
-__device__ void prefix_part(const CachedArgs& a, uint8_t* lds, int block, int wave, int lane) {
+__device__ __forceinline__ void prefix_part(const CachedArgs& a, uint8_t* buf0, uint8_t* buf1, int block, int wave, int lane) {
     using T = Tile<D>;
     constexpr int kTileB = kPrefixTile * T::kRowB;
     constexpr int kDma = kTileB / 1024 / kCW;
@@ -146,13 +158,14 @@ __device__ void prefix_part(const CachedArgs& a, uint8_t* lds, int block, int wa
     const int tiles = (k1 - k0 + kPrefixTile - 1) / kPrefixTile;
     const bool busy = x - c < rows;              // the wave has a row
 
-    auto rows_of = [&](int t) { return pool_row(a, a.prefix_pages, min(k0 + t * kPrefixTile + lane, k1 - 1)); };
+    auto key_of = [&](int t) { return min(k0 + t * kPrefixTile + lane, k1 - 1); };
+    auto page_of = [&](int t) { return a.prefix_pages[key_of(t) >> a.page_shift]; };
     auto issue = [&](uint8_t* buf, uint32_t pr) {
         copy_paged<D, kDma>(a.k + (int64_t)kvh * D, a.kv_stride, pr, buf, wave * kDma, lane);
         copy_paged<D, kDma>(a.v + (int64_t)kvh * D, a.kv_stride, pr, buf + kTileB, wave * kDma, lane);
     };
-    issue(lds, rows_of(0));
-    uint32_t next = rows_of(min(1, tiles - 1));
+    issue(buf0, pool_row(a, page_of(0), key_of(0)));
+    int32_t next = page_of(min(1, tiles - 1));
 
     const QueryRow q = query_row(a, G, kvh, min(x, rows - 1));
     bf16x8 qf[D / 16];
@@ -161,173 +174,244 @@ __device__ void prefix_part(const CachedArgs& a, uint8_t* lds, int block, int wa
     const float cs = a.scale * kLog2e;
     Rows<D> r;
     r.clear();
-    for (int t = 0; t < tiles; ++t) {
-        uint8_t* cur = lds + (t & 1) * 2 * kTileB;
+    auto step = [&](const uint8_t* cur, uint8_t* other, int t) {
         wait_vm<0>();
         stage_barrier();
         if (t + 1 < tiles) {
-            issue(lds + ((t + 1) & 1) * 2 * kTileB, next);
-            next = rows_of(min(t + 2, tiles - 1));
+            issue(other, pool_row(a, next, key_of(t + 1)));
+            next = page_of(min(t + 2, tiles - 1));
         }
         const int seen = k1 - 1 - k0 - t * kPrefixTile;
         if (busy) attend<D, kPrefixTile>(r, qf, cur, cur + kTileB, lo, cs, seen < kPrefixTile - 1, seen, h);
+    };
+    for (int t = 0; t < tiles; t += 2) {
+        step(buf0, buf1, t);
+        if (t + 1 < tiles) step(buf1, buf0, t + 1);
     }
     const float l = sum_halves(r.l);
     if (x < rows) store_part<D>(a, split, q, r, l, h);
 }
 
-// The suffix keys of one sequence for 32 of its rows of one head: the waves
-// take every kCW-th tile, each with its own staging buffer, and join through LDS.
-template <int D>
-__device__ void suffix_part(const CachedArgs& a, uint8_t* lds, int block, int wave, int lane) {
+// Keys of one sequence for 32 of its rows of one head: its own (kDirect: the
+// prefix's as well).  The W waves take every W-th tile of KT keys, each with a
+// staging buffer of its own, and join through LDS: wave w then adds up pieces
+// w, w + W, .. (4 values of each row) of all waves.  kDirect, or the only
+// split of all keys: the sum is the output; else it is left in the workspace.
+template <int D, int W, int KT, bool kDirect>
+__device__ __forceinline__ void own_part(const CachedArgs& a, uint8_t* buf0, uint8_t* buf1, float (*ml)[2][64], int block,
+                                         int wave, int lane) {
     using T = Tile<D>;
-    constexpr int KT = kSuffixTile<D>;
-    constexpr int kTileB = KT * T::kRowB;        // 8 KiB
+    constexpr int kTileB = KT * T::kRowB;
+    constexpr int kWaveB = 2 * kTileB;
+    static_assert(kWaveB >= D * 32 * 4, "a wave's o fits its staging buffer");
     const int c = lane & 31, h = lane >> 5, G = a.Hq / a.Hkv;
     const int kvh = block % a.Hkv;
     int rest = block / a.Hkv;
-    const int split = rest % a.suffix_splits;
-    rest /= a.suffix_splits;
+    const int splits = kDirect ? 1 : a.suffix_splits, split = rest % splits;
+    rest /= splits;
     const int blocks = (a.L * G + 31) / 32;
     const int seq = rest / blocks, rb = rest % blocks;
     const int32_t* pages = a.page_table + (int64_t)seq * a.max_pages;
     const int len = min(max(a.suffix_len[seq], 0), a.max_pages << a.page_shift);
-    const int all = (len + KT - 1) / KT, per = (all + a.suffix_splits - 1) / a.suffix_splits;
+    const int prefix = kDirect ? a.prefix_len : 0, pt = (prefix + KT - 1) / KT;     // tiles of the prefix come first
+    const int all = pt + (len + KT - 1) / KT, per = (all + splits - 1) / splits;
     const int t0 = min(split * per, all), t1 = min(t0 + per, all);
 
     const int y = rb * 32 + c;                   // row among the sequence's L * G
     const bool exists = y < a.L * G;
     const QueryRow q = query_row(a, G, kvh, (int64_t)seq * a.L * G + min(y, a.L * G - 1));
-    const int last = len - a.L + min(y, a.L * G - 1) / G;    // the row's last visible key
-    bf16x8 qf[D / 16];
-    load_row_operand<D>(qf, a.q + q.token * a.q_stride + (int64_t)q.head * D, h, exists);
+    const int last = len - a.L + min(y, a.L * G - 1) / G;    // the row's last visible own key
     const LaneOffsets<D> lo(lane);
     const float cs = a.scale * kLog2e;
     Rows<D> r;
     r.clear();
-    uint8_t* buf = lds + wave * 2 * kTileB;
-    auto rows_of = [&](int t) { return pool_row(a, pages, min(t * KT + lane % KT, len - 1)); };
+    auto region = [&](int w) { return (w < W / 2 ? buf0 : buf1) + (w % (W / 2)) * kWaveB; };
+    uint8_t* buf = region(wave);
+    auto key_of = [&](int t) {
+        return kDirect && t < pt ? min(t * KT + lane % KT, prefix - 1) : min((t - pt) * KT + lane % KT, len - 1);
+    };
+    auto page_of = [&](int t) { return (kDirect && t < pt ? a.prefix_pages : pages)[key_of(t) >> a.page_shift]; };
     const int mine = t0 + wave;
-    if (mine < t1) {
-        uint32_t cur = rows_of(mine);
-        for (int t = mine; t < t1; t += kCW) {
-            copy_paged<D, kTileB / 1024>(a.k + (int64_t)kvh * D, a.kv_stride, cur, buf, 0, lane);
-            copy_paged<D, kTileB / 1024>(a.v + (int64_t)kvh * D, a.kv_stride, cur, buf + kTileB, 0, lane);
-            if (t + kCW < t1) cur = rows_of(t + kCW);
-            wait_vm<0>();
-            attend<D, KT>(r, qf, buf, buf + kTileB, lo, cs, t * KT + KT - 1 > len - a.L, last - t * KT, h);
-        }
+    int32_t next = mine < t1 ? page_of(mine) : 0;
+    bf16x8 qf[D / 16];
+    load_row_operand<D>(qf, a.q + q.token * a.q_stride + (int64_t)q.head * D, h, exists);
+    for (int t = mine; t < t1; t += W) {
+        const uint32_t cur = pool_row(a, next, key_of(t));
+        copy_paged<D, kTileB / 1024>(a.k + (int64_t)kvh * D, a.kv_stride, cur, buf, 0, lane);
+        copy_paged<D, kTileB / 1024>(a.v + (int64_t)kvh * D, a.kv_stride, cur, buf + kTileB, 0, lane);
+        if (t + W < t1) next = page_of(t + W);
+        wait_vm<0>();
+        asm volatile("" ::: "memory");
+        const int k0 = (t - pt) * KT;            // first own key of the tile; negative: a tile of the prefix
+        if (kDirect && t < pt) attend<D, KT>(r, qf, buf, buf + kTileB, lo, cs, t * KT + KT > prefix, prefix - 1 - t * KT, h);
+        else attend<D, KT>(r, qf, buf, buf + kTileB, lo, cs, k0 + KT - 1 > len - a.L, last - k0, h);
     }
-    // join the waves: their m, l and o in LDS, then wave 0 adds them up
     const float l = sum_halves(r.l);
     lds_barrier();
-    float* fo = reinterpret_cast<float*>(lds);                   // [wave][D / 32 * 4][64 lanes][4]
-    float* fm = fo + (kCW - 1) * D * 32;
-    if (wave > 0) {
-        float* p = fo + (wave - 1) * D * 32;
-#pragma unroll
-        for (int b = 0; b < D / 32; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; i += 4)
-                *reinterpret_cast<float4*>(p + ((b * 4 + i / 4) * 64 + lane) * 4) =
-                    make_float4(r.o[b][i], r.o[b][i + 1], r.o[b][i + 2], r.o[b][i + 3]);
-        fm[(wave - 1) * 128 + lane] = r.m;
-        fm[(wave - 1) * 128 + 64 + lane] = l;
-    }
-    lds_barrier();
-    if (wave > 0) return;
-    float top = r.m, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < kCW - 1; ++w) top = fmaxf(top, fm[w * 128 + lane]);
-    const float ref = top == kNegInf ? 0.f : top;
-    const float own = exp2_fast(r.m - ref);
-    sum = own * l;
+    float* mine_o = reinterpret_cast<float*>(buf);               // [D / 8 pieces][64 lanes][4]
 #pragma unroll
     for (int b = 0; b < D / 32; ++b)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) r.o[b][i] *= own;
+        for (int i = 0; i < 16; i += 4)
+            *reinterpret_cast<float4*>(mine_o + ((b * 4 + i / 4) * 64 + lane) * 4) =
+                make_float4(r.o[b][i], r.o[b][i + 1], r.o[b][i + 2], r.o[b][i + 3]);
+    ml[wave][0][lane] = r.m;
+    ml[wave][1][lane] = l;
+    lds_barrier();
+    float top = kNegInf, sum = 0.f, f[W];
 #pragma unroll
-    for (int w = 0; w < kCW - 1; ++w) {
-        const float f = exp2_fast(fm[w * 128 + lane] - ref);
-        sum += f * fm[w * 128 + 64 + lane];
+    for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w][0][lane]);
+    const float ref = top == kNegInf ? 0.f : top;
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b)
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const float4 v = *reinterpret_cast<const float4*>(fo + w * D * 32 + ((b * 4 + i / 4) * 64 + lane) * 4);
-                r.o[b][i] += f * v.x; r.o[b][i + 1] += f * v.y; r.o[b][i + 2] += f * v.z; r.o[b][i + 3] += f * v.w;
-            }
+    for (int w = 0; w < W; ++w) {
+        f[w] = exp2_fast(ml[w][0][lane] - ref);
+        sum += f[w] * ml[w][1][lane];
     }
-    r.m = top;
-    if (exists) store_part<D>(a, a.prefix_splits + split, q, r, sum, h);
+    const bool whole = kDirect || a.prefix_splits + splits == 1;
+    // no visible key: 0; a NaN stays
+    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    const int64_t at = ((int64_t)(a.prefix_splits + split) * a.N * a.L + q.token) * a.Hq + q.head;
+#pragma unroll
+    for (int g = wave; g < D / 8; g += W) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float4 v = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(region(w)) + (g * 64 + lane) * 4);
+            x.x = __builtin_fmaf(f[w], v.x, x.x);
+            x.y = __builtin_fmaf(f[w], v.y, x.y);
+            x.z = __builtin_fmaf(f[w], v.z, x.z);
+            x.w = __builtin_fmaf(f[w], v.w, x.w);
+        }
+        const int col = 8 * g + 4 * h;           // values 32 b + 8 (i / 4) + 4 h ..
+        if (!exists) continue;
+        if (whole) {
+            *reinterpret_cast<uint2*>(a.out + q.token * a.out_stride + (int64_t)q.head * D + col) =
+                make_uint2(Elem<uint16_t>::pack2(x.x * inv, x.y * inv), Elem<uint16_t>::pack2(x.z * inv, x.w * inv));
+        } else {
+            *reinterpret_cast<float4*>(a.part_o + at * D + col) = x;
+        }
+    }
+    if (!whole && exists && wave == 0 && h == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(top, sum);
 }
 
+// Split form: the prefix's workgroups first, which run longest, then the
+// suffixes'.
 template <int D>
-__global__ __launch_bounds__(64 * kCW, 2) void attn_cached_kernel(CachedArgs a) {
-    constexpr int kPrefixB = 2 * 2 * kPrefixTile * 2 * D;                       // two tiles of K and V
-    constexpr int kSuffixB = kCW * 2 * 8192;                                    // a tile of K and V per wave
-    constexpr int kJoinB = (kCW - 1) * (D * 32 + 128) * 4;
-    constexpr int kA = kPrefixB > kSuffixB ? kPrefixB : kSuffixB;
-    __shared__ __attribute__((aligned(1024))) uint8_t lds[kA > kJoinB ? kA : kJoinB];
+__global__ __launch_bounds__(64 * kCW, D == 64 ? 4 : 2) void attn_cached_kernel(CachedArgs a) {
+    constexpr int kBufB = 2 * kPrefixTile * Tile<D>::kRowB;
+    static_assert(kBufB == 2 * 2 * kOwnTile * Tile<D>::kRowB, "two waves' staging per buffer");
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[kBufB], buf1[kBufB];
+    __shared__ float ml[kCW][2][64];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    if ((int)blockIdx.x < a.prefix_blocks) prefix_part<D>(a, lds, blockIdx.x, wave, lane);
-    else suffix_part<D>(a, lds, blockIdx.x - a.prefix_blocks, wave, lane);
+    const int b = blockIdx.x, p = (int)a.prefix_blocks;
+    if (b < p) prefix_part<D>(a, buf0, buf1, b, wave, lane);
+    else own_part<D, kCW, kOwnTile, false>(a, buf0, buf1, ml, b - p, wave, lane);
 }
 
-// Joins the splits: D / 4 lanes per (token row, head).
+// Direct form, for few keys: one workgroup per sequence, head and 32 rows reads
+// prefix and suffix and writes the output.
+template <int D>
+__global__ __launch_bounds__(64 * kDirectW) void attn_cached_direct_kernel(CachedArgs a) {
+    constexpr int KT = 4096 / D, kBufB = kDirectW / 2 * 2 * KT * Tile<D>::kRowB;
+    __shared__ __attribute__((aligned(1024))) uint8_t buf0[kBufB], buf1[kBufB];
+    __shared__ float ml[kDirectW][2][64];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    own_part<D, kDirectW, KT, true>(a, buf0, buf1, ml, blockIdx.x, wave, threadIdx.x & 63);
+}
+
+// Joins the splits: a wave per (token row, head).  First every lane takes a
+// split's m and l, then D / 4 lanes times 256 / D groups of them add up o.
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(CachedArgs a) {
-    constexpr int kLanes = D / 4;
+    constexpr int kLanes = D / 4, kGroups = 64 / kLanes;
     const int64_t rows = (int64_t)a.N * a.L * a.Hq;
-    const int64_t row = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;
-    const int j = threadIdx.x % kLanes;
+    const int64_t row = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63, j = lane % kLanes, g = lane / kLanes;
     if (row >= rows) return;
     const int splits = a.prefix_splits + a.suffix_splits;
     float m = kNegInf, l = 0.f;
     float o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < splits; ++s) {
-        const int64_t at = s * rows + row;
-        const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
-        const float4 x = *reinterpret_cast<const float4*>(a.part_o + at * D + 4 * j);
-        const float mn = fmaxf(m, ml.x), ref = mn == kNegInf ? 0.f : mn;
-        const float f0 = exp2_fast(m - ref), f1 = exp2_fast(ml.x - ref);
+    for (int s0 = 0; s0 < splits; s0 += 64) {
+        float2 ml = make_float2(kNegInf, 0.f);
+        if (s0 + lane < splits) ml = *reinterpret_cast<const float2*>(a.part_ml + ((s0 + lane) * rows + row) * 2);
+        float mn = ml.x;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) mn = fmaxf(mn, __shfl_xor(mn, d, 64));
+        mn = fmaxf(mn, m);
+        const float ref = mn == kNegInf ? 0.f : mn;
+        const float f = exp2_fast(ml.x - ref), old = exp2_fast(m - ref);
+        float sum = f * ml.y;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
         m = mn;
-        l = l * f0 + ml.y * f1;
-        o[0] = o[0] * f0 + x.x * f1;
-        o[1] = o[1] * f0 + x.y * f1;
-        o[2] = o[2] * f0 + x.z * f1;
-        o[3] = o[3] * f0 + x.w * f1;
+        l = l * old + sum;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] *= old;
+        const int n = min(64, splits - s0);
+        for (int s = 0; s < n; s += kGroups) {
+            const float w = __shfl(f, s + g, 64);
+            if (s + g < n) {
+                const float4 x = *reinterpret_cast<const float4*>(a.part_o + ((s0 + s + g) * rows + row) * D + 4 * j);
+                o[0] = __builtin_fmaf(w, x.x, o[0]);
+                o[1] = __builtin_fmaf(w, x.y, o[1]);
+                o[2] = __builtin_fmaf(w, x.z, o[2]);
+                o[3] = __builtin_fmaf(w, x.w, o[3]);
+            }
+        }
     }
-    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);      // no visible key: 0; NaN stays
+#pragma unroll
+    for (int d = kLanes; d < 64; d <<= 1)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += __shfl_xor(o[i], d, 64);
+    const float inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);      // no visible key: 0; a NaN stays
     uint2 v;
     v.x = Elem<uint16_t>::pack2(o[0] * inv, o[1] * inv);
     v.y = Elem<uint16_t>::pack2(o[2] * inv, o[3] * inv);
-    *reinterpret_cast<uint2*>(a.out + row / a.Hq * a.out_stride + (row % a.Hq) * D + 4 * j) = v;
+    if (g == 0) *reinterpret_cast<uint2*>(a.out + row / a.Hq * a.out_stride + (row % a.Hq) * D + 4 * j) = v;
 }
 
-// Splits.  The card has 256 CUs, two workgroups each: the prefix gets as many
-// splits of at least 64 keys as one round of 512 workgroups holds, the suffixes
-// as many of at least one tile per wave as two rounds hold.
+// The direct form where a workgroup per (sequence, head) covers all keys in two
+// rounds of its waves and the card holds them all at once (one sequence, 32 / 8
+// heads of 64, prefix 500, suffix 37: 6.0 us, split 7.1; at 1000 + 100 keys 7.6
+// and 7.5; 64 sequences of 64 keys: 8.0 and 4.8).
+//
+// Splits of the split form: the prefix gets workgroups of at least 64 keys, one
+// per CU where the suffixes' bytes take longer than the prefix's products (the
+// rest of the CU reads suffixes meanwhile), two where they do not; the suffixes
+// as many of at least a tile per wave as two rounds of 512 hold.  Measured with
+// 1 / 2 / 4 prefix workgroups per CU: 256 sequences, 4096 + 600 keys, 32 / 8 heads
+// of 64: 59 / 64 / 74 us; 64 x 8 rows, 16384 + 999 keys: 206 / 129 / 121 us, with 40
+// / 8 heads of 128: 524 / 241 / 251 us.
 CachedPlan cached_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_keys) {
     CachedPlan p;
     const int G = Hq / Hkv;
     const int64_t rows = (int64_t)N * L * G;
     const int64_t row_blocks = (rows + kCRows - 1) / kCRows;
+    const int64_t base = (int64_t)N * ((L * G + 31) / 32) * Hkv;
     p.prefix_splits = 0;
     p.prefix_chunk = 0;
     p.prefix_blocks = 0;
+    const int KT = 4096 / D;
+    const int64_t rounds = ((prefix_len + KT - 1) / KT + (max_keys + KT - 1) / KT + kDirectW - 1) / kDirectW;
+    p.direct = base <= 256 && rounds <= 2;
+    if (p.direct) {
+        p.suffix_splits = 0;
+        p.suffix_blocks = base;
+        return p;
+    }
     if (prefix_len > 0) {
         const int tiles = (prefix_len + kPrefixTile - 1) / kPrefixTile;
-        const int64_t want = 512 / (row_blocks * Hkv);
+        // seconds at 5e12 bytes/s and 8e14 flops/s; a batch fills about half of its page tables
+        const double read = 2. * N * max_keys * Hkv * D / 5e12, product = 4. * rows * Hkv * D * prefix_len / 8e14;
+        const int64_t want = (read > product ? 256 : 512) / (row_blocks * Hkv);
         const int splits = (int)(want < 1 ? 1 : want < tiles ? want : tiles);
         const int per = (tiles + splits - 1) / splits;
         p.prefix_chunk = per * kPrefixTile;
         p.prefix_splits = (tiles + per - 1) / per;
         p.prefix_blocks = row_blocks * Hkv * p.prefix_splits;
     }
-    const int64_t base = (int64_t)N * ((L * G + 31) / 32) * Hkv;
-    const int64_t per_wg = (int64_t)kCW * 4096 / D;
+    const int64_t per_wg = (int64_t)kCW * kOwnTile;
     const int64_t most = (max_keys + per_wg - 1) / per_wg, want = 1024 / base;
     p.suffix_splits = (int)(want < 1 ? 1 : want < most ? want : most);
     if (p.suffix_splits < 1) p.suffix_splits = 1;
@@ -336,12 +420,17 @@ CachedPlan cached_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int
 }
 
 template <int D>
-static hipError_t launch_cached(const CachedArgs& a, int64_t suffix_blocks, hipStream_t s) {
-    const int64_t blocks = a.prefix_blocks + suffix_blocks;
-    const int64_t joins = ((int64_t)a.N * a.L * a.Hq * (D / 4) + 255) / 256;
+static hipError_t launch_cached(const CachedArgs& a, const CachedPlan& p, hipStream_t s) {
+    const int64_t blocks = p.prefix_blocks + p.suffix_blocks;
+    const int64_t joins = ((int64_t)a.N * a.L * a.Hq + 3) / 4;
     if (blocks >= ((int64_t)1 << 31) || joins >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+    if (p.direct) {
+        hipLaunchKernelGGL((attn_cached_direct_kernel<D>), dim3((uint32_t)blocks), dim3(64 * kDirectW), 0, s, a);
+        return hipGetLastError();
+    }
     hipLaunchKernelGGL((attn_cached_kernel<D>), dim3((uint32_t)blocks), dim3(64 * kCW), 0, s, a);
-    hipLaunchKernelGGL((attn_join_kernel<D>), dim3((uint32_t)joins), dim3(256), 0, s, a);
+    if (p.prefix_splits + p.suffix_splits > 1)
+        hipLaunchKernelGGL((attn_join_kernel<D>), dim3((uint32_t)joins), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
@@ -351,7 +440,7 @@ hipError_t launch_attn_cached(CachedArgs a, int D, hipStream_t s) {
     a.prefix_chunk = p.prefix_chunk;
     a.prefix_blocks = p.prefix_blocks;
     a.suffix_splits = p.suffix_splits;
-    return D == 64 ? launch_cached<64>(a, p.suffix_blocks, s) : launch_cached<128>(a, p.suffix_blocks, s);
+    return D == 64 ? launch_cached<64>(a, p, s) : launch_cached<128>(a, p, s);
 }
 
 }  // namespace lfm2sc

@@ -49,6 +49,7 @@ struct CachedArgs {
     int64_t prefix_blocks;                            // the number of prefix workgroups
 };
 struct CachedPlan {
+    bool direct;                         // one workgroup per sequence, head and 32 rows; no workspace
     int prefix_splits, prefix_chunk, suffix_splits;
     int64_t prefix_blocks, suffix_blocks;
 };

@@ -88,8 +88,8 @@ int lfm2sc_attn_backward(int dtype, int D, int num_heads, int num_kv_heads,
                          void* workspace, size_t workspace_bytes, void* stream);
 
 /*
- * Bytes of workspace lfm2sc_attn_cached needs; 0 for invalid sizes (and when
- * num_seqs or L is 0).
+ * Bytes of workspace lfm2sc_attn_cached needs; 0 for invalid sizes, when num_seqs
+ * or L is 0, and for few keys, which need none (workspace may then be NULL).
  */
 size_t lfm2sc_attn_cached_workspace_bytes(int dtype, int D, int num_heads, int num_kv_heads, int num_seqs, int L,
                                           int prefix_len, int max_pages, int page_size);

@@ -87,7 +87,7 @@ def test_backward_no_work_and_workspace(L):
         assert need(*bad) == 0, bad
 
 
-CACHED = dict(dtype=0, D=64, Hq=8, Hkv=2, q=P, qs=512, N=3, Lb=2, k=P, v=P, kvs=128, pages=10, page=16, pp=P, plen=20, table=P,
+CACHED = dict(dtype=0, D=64, Hq=8, Hkv=2, q=P, qs=512, N=3, Lb=2, k=P, v=P, kvs=128, pages=10, page=16, pp=P, plen=2000, table=P,
               most=4, lens=P, scale=0.125, out=P, os=512, ws=P, ws_bytes=1 << 30, stream=None)
 
 
@@ -115,7 +115,7 @@ def test_cached_no_work_and_workspace(L):
     assert _cached(L, N=0, q=None, k=None, out=None, ws=None) == OK
     assert _cached(L, Lb=0, q=None, k=None, out=None, ws=None) == OK
     need = L.lfm2sc_attn_cached_workspace_bytes
-    assert need(0, 64, 8, 2, 3, 2, 20, 4, 16) > 0
+    assert need(0, 64, 8, 2, 3, 2, 2000, 4, 16) > 0
     for bad in ((1, 64, 8, 2, 3, 2, 20, 4, 16), (0, 64, 8, 3, 3, 2, 20, 4, 16), (0, 64, 8, 2, 0, 2, 20, 4, 16),
                 (0, 64, 8, 2, 3, 0, 20, 4, 16), (0, 64, 8, 2, 3, 2, -1, 4, 16), (0, 64, 8, 2, 3, 2, 20, 4, 17),
                 (0, 64, 8, 2, 3, 2, 20, -4, 16)):
