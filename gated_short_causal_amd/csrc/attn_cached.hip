@@ -65,9 +65,11 @@ struct Rows {
 // One staged tile of KT keys against the wave's rows.  If `masked` (uniform),
 // keys numbered above `seen`, the lane's row's last visible key within the
 // tile, are masked.  A row that has seen no key keeps m = -inf and o = l = 0.
-template <int D, int KT>
+// after_k runs when the K tile has been read, before_v before the V tile is.
+template <int D, int KT, typename F1, typename F2>
 __device__ __forceinline__ void attend(Rows<D>& r, const bf16x8 (&qf)[D / 16], const uint8_t* kb, const uint8_t* vb,
-                                       const LaneOffsets<D>& lo, float cs, bool masked, int seen, int h) {
+                                       const LaneOffsets<D>& lo, float cs, bool masked, int seen, int h, F1 after_k,
+                                       F2 before_v) {
     using T = Tile<D>;
     f32x16 s[KT / 32];
 #pragma unroll
@@ -77,6 +79,7 @@ __device__ __forceinline__ void attend(Rows<D>& r, const bf16x8 (&qf)[D / 16], c
 #pragma unroll
         for (int ds = 0; ds < D / 16; ++ds) s[n] = mfma32(lds_row(kb + n * 32 * T::kRowB, lo.row[ds]), qf[ds], s[n]);
     }
+    after_k();
     if (masked) {
 #pragma unroll
         for (int n = 0; n < KT / 32; ++n)
@@ -109,6 +112,7 @@ __device__ __forceinline__ void attend(Rows<D>& r, const bf16x8 (&qf)[D / 16], c
             sum += s[n][i];
         }
     r.l += sum;
+    before_v();
 #pragma unroll
     for (int n = 0; n < KT / 32; ++n)
 #pragma unroll
@@ -182,7 +186,7 @@ __device__ __forceinline__ void prefix_part(const CachedArgs& a, uint8_t* buf0, 
             next = page_of(min(t + 2, tiles - 1));
         }
         const int seen = k1 - 1 - k0 - t * kPrefixTile;
-        if (busy) attend<D, kPrefixTile>(r, qf, cur, cur + kTileB, lo, cs, seen < kPrefixTile - 1, seen, h);
+        if (busy) attend<D, kPrefixTile>(r, qf, cur, cur + kTileB, lo, cs, seen < kPrefixTile - 1, seen, h, [] {}, [] {});
     };
     for (int t = 0; t < tiles; t += 2) {
         step(buf0, buf1, t);
@@ -226,29 +230,58 @@ __device__ __forceinline__ void own_part(const CachedArgs& a, uint8_t* buf0, uin
     Rows<D> r;
     r.clear();
     auto region = [&](int w) { return (w < W / 2 ? buf0 : buf1) + (w % (W / 2)) * kWaveB; };
-    uint8_t* buf = region(wave);
+    uint8_t* kb = buf0 + wave * kTileB;
+    uint8_t* vb = buf1 + wave * kTileB;
     auto key_of = [&](int t) {
         return kDirect && t < pt ? min(t * KT + lane % KT, prefix - 1) : min((t - pt) * KT + lane % KT, len - 1);
     };
     auto page_of = [&](int t) { return (kDirect && t < pt ? a.prefix_pages : pages)[key_of(t) >> a.page_shift]; };
+    // The wave's next K tile is copied as soon as the scores of this one are formed, the next V tile after the
+    // products with this one, and the page numbers a tile before that; so its waits leave the copies issued later in
+    // flight.  Order of its vector memory operations: pages(t + 1), K(t), V(t), [pages(t + 2), K(t + 1)], V(t + 1), ..
+    constexpr int kN = kTileB / 1024;
+    const uint16_t* kp = a.k + (int64_t)kvh * D;
+    const uint16_t* vp = a.v + (int64_t)kvh * D;
     const int mine = t0 + wave;
-    int32_t next = mine < t1 ? page_of(mine) : 0;
     bf16x8 qf[D / 16];
     load_row_operand<D>(qf, a.q + q.token * a.q_stride + (int64_t)q.head * D, h, exists);
-    for (int t = mine; t < t1; t += W) {
-        const uint32_t cur = pool_row(a, next, key_of(t));
-        copy_paged<D, kTileB / 1024>(a.k + (int64_t)kvh * D, a.kv_stride, cur, buf, 0, lane);
-        copy_paged<D, kTileB / 1024>(a.v + (int64_t)kvh * D, a.kv_stride, cur, buf + kTileB, 0, lane);
-        if (t + W < t1) next = page_of(t + W);
-        wait_vm<0>();
+    int32_t next = 0;
+    uint32_t rows = 0;
+    if (mine < t1) {
+        rows = pool_row(a, page_of(mine), key_of(mine));
+        next = page_of(min(mine + W, t1 - 1));
+        copy_paged<D, kN>(kp, a.kv_stride, rows, kb, 0, lane);
+        copy_paged<D, kN>(vp, a.kv_stride, rows, vb, 0, lane);
+    }
+    auto tile = [&](auto more_c, int t) {        // more: the wave has another tile after this one
+        constexpr bool more = decltype(more_c)::value;
+        wait_vm<kN>();
         asm volatile("" ::: "memory");
+        auto after_k = [&] {
+            if constexpr (more) {
+                rows = pool_row(a, next, key_of(t + W));
+                next = page_of(min(t + 2 * W, t1 - 1));
+                copy_paged<D, kN>(kp, a.kv_stride, rows, kb, 0, lane);
+            }
+        };
+        auto before_v = [&] {
+            wait_vm<more ? kN + 1 : 0>();
+            asm volatile("" ::: "memory");
+        };
         const int k0 = (t - pt) * KT;            // first own key of the tile; negative: a tile of the prefix
-        if (kDirect && t < pt) attend<D, KT>(r, qf, buf, buf + kTileB, lo, cs, t * KT + KT > prefix, prefix - 1 - t * KT, h);
-        else attend<D, KT>(r, qf, buf, buf + kTileB, lo, cs, k0 + KT - 1 > len - a.L, last - k0, h);
+        const bool shared = kDirect && t < pt;
+        attend<D, KT>(r, qf, kb, vb, lo, cs, shared ? t * KT + KT > prefix : k0 + KT - 1 > len - a.L,
+                      shared ? prefix - 1 - t * KT : last - k0, h, after_k, before_v);
+        if constexpr (more) copy_paged<D, kN>(vp, a.kv_stride, rows, vb, 0, lane);
+    };
+    if (mine < t1) {
+        int t = mine;
+        for (; t + W < t1; t += W) tile(std::true_type{}, t);
+        tile(std::false_type{}, t);
     }
     const float l = sum_halves(r.l);
     lds_barrier();
-    float* mine_o = reinterpret_cast<float*>(buf);               // [D / 8 pieces][64 lanes][4]
+    float* mine_o = reinterpret_cast<float*>(region(wave));      // [D / 8 pieces][64 lanes][4]
 #pragma unroll
     for (int b = 0; b < D / 32; ++b)
 #pragma unroll
