@@ -313,7 +313,6 @@ int lfm2sc_accept_drafts(int dtype, int V, int num_seqs, int L, const void* targ
         a.u_accept = u_accept; a.u_sample = u_sample;
         a.accept_len = accept_len; a.keep_len = keep_len; a.next_token = next_token;
         a.sums = static_cast<double*>(workspace);
-        a.chunk = 0;
         return launched(fn, launch_drafts(a, s));
     };
     if (dtype == LFM2SC_BF16) {

@@ -65,9 +65,8 @@ struct DraftArgs {
     const float* u_accept; const float* u_sample;
     int32_t* accept_len; int32_t* keep_len; int32_t* next_token;
     double* sums;                                // workspace [N][2][chunks]
-    int chunk;                                   // tokens per chunk; set by the launcher
 };
-constexpr int kDraftChunk = 4096;
+constexpr int kDraftChunk = 4096;                // tokens per chunk of the split form
 int draft_chunks(int V);
 
 // Host check of int32 device data (check.hip): n entries within [lo, hi].
@@ -82,6 +81,6 @@ int attn_backward_splits(int Hq, int Hkv, int64_t total_T, int N);
 hipError_t launch_attn_backward(const AttnGradArgs& a, int D, hipStream_t s);
 hipError_t launch_attn_cached(CachedArgs a, int D, hipStream_t s);
 template <typename E>
-hipError_t launch_drafts(DraftArgs<E> a, hipStream_t s);
+hipError_t launch_drafts(const DraftArgs<E>& a, hipStream_t s);
 
 }  // namespace lfm2sc

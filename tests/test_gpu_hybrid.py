@@ -63,7 +63,7 @@ def _untouched(x, rows):
 PROMPTS = [
     ([1], 1, 1, 64), ([1], 8, 2, 128), ([2, 1, 3], 4, 1, 64), ([63], 2, 2, 64), ([64], 2, 1, 128), ([65], 2, 1, 64),
     ([127, 1, 0, 128, 0], 4, 2, 64), ([129, 31, 97], 6, 2, 128), ([256], 4, 4, 64), ([257, 255], 3, 1, 64),
-    ([500], 5, 5, 128), ([300, 2], 12, 1, 64), ([3] * 70 + [150] + [1] * 65, 2, 1, 64), ([700], 9, 3, 128), ([1111], 2, 1, 64),
+    ([500], 5, 5, 128), ([300, 2], 12, 1, 64), ([65] * 128, 16, 8, 64), ([33] * 260, 16, 8, 128), ([3] * 70 + [150] + [1] * 65, 2, 1, 64), ([700], 9, 3, 128), ([1111], 2, 1, 64),
 ]
 
 
@@ -229,6 +229,10 @@ CACHED = [
     ([130] * 40, 1, 129, 32, 4, 4, 64), ([7, 31, 3], 3, 1000, 128, 5, 5, 128), ([0, 2, 5], 3, 0, 4, 4, 2, 64),
     ([0, 1, 0], 1, 0, 16, 4, 2, 128), ([0, 0], 2, 40, 16, 4, 2, 64), ([700, 1], 2, 300, 16, 2, 1, 64), ([2000], 1, 0, 64, 16, 2, 128),
     ([60] * 9, 5, 3000, 16, 8, 1, 64),
+    # more workgroups than CUs, so never the direct form; without a prefix a single split writes the output itself
+    ([0, 1, 300, 64, 65] * 30, 1, 700, 16, 4, 2, 64), ([0, 3, 130] * 30, 3, 0, 32, 8, 4, 128), ([1, 257] * 40, 1, 33, 8, 8, 8, 128),
+    # the prefix's chunks end inside a tile
+    ([2, 40], 2, 4500, 32, 8, 2, 64), ([9], 1, 6007, 1, 2, 1, 128),
 ]
 
 
@@ -328,7 +332,8 @@ def _check_drafts(*args, num_drafts=None):
 
 
 @pytest.mark.parametrize("N,L,V,pad", [(1, 1, 1, 0), (3, 2, 7, 1), (5, 7, 8, 0), (2, 0, 100, 3), (4, 64, 33, 0), (9, 4, 2048, 0),
-                                       (3, 4, 4097, 0), (70, 3, 1000, 5), (2, 8, 32003, 0), (1, 5, 65536, 8)])
+                                       (3, 4, 4097, 0), (70, 3, 1000, 5), (2, 8, 32003, 0), (1, 5, 65536, 8),
+                                       (40, 2, 8193, 0), (3, 3, 70001, 0), (2, 1, 131072, 1), (34, 1, 66001, 0), (1, 1, 600000, 0)])
 @pytest.mark.parametrize("dtype", [torch.float32, BF])
 @pytest.mark.parametrize("with_draft", [True, False])
 def test_drafts(N, L, V, pad, dtype, with_draft):
@@ -336,14 +341,15 @@ def test_drafts(N, L, V, pad, dtype, with_draft):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, BF])
-def test_drafts_borders(dtype):
+@pytest.mark.parametrize("V", [5000, 70000])
+def test_drafts_borders(dtype, V):
     """u of 0, of just below 1 and outside [0, 1); a NaN u; drafts outside the vocabulary; ragged numbers of drafts."""
-    target, draft, tokens, ua, us = _draft_case(12, 3, 5000, dtype, True, seed=8)
+    target, draft, tokens, ua, us = _draft_case(12, 3, V, dtype, True, seed=8)
     us[:6] = torch.tensor([0.0, 1 - 2 ** -24, 1.0, 2.0, -1.0, float("nan")])
     ua[6] = 0.0
     ua[7] = 1.0
     ua[8, 1] = float("nan")
-    tokens[9, 0], tokens[10, 1], tokens[11, 2] = -1, 5000, 1 << 30
+    tokens[9, 0], tokens[10, 1], tokens[11, 2] = -1, V, 1 << 30
     ua[10, 0], ua[11, :2] = 0.0, 0.0
     _check_drafts(target, draft, tokens, ua, us)
     _check_drafts(target, None, tokens, ua, us)
@@ -351,7 +357,7 @@ def test_drafts_borders(dtype):
     _check_drafts(target, draft, tokens, ua, us, num_drafts=nd)
 
 
-@pytest.mark.parametrize("V", [16, 9001])
+@pytest.mark.parametrize("V", [16, 9001, 80003])
 def test_drafts_degenerate_rows(V):
     """p = q (nothing left: drawn from p), one-hot rows, all-zero rows, NaN and negative entries, flat rows with the
     border on a token's edge."""
