@@ -50,9 +50,8 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnGradArgs a) {
 // dk (kK) and dv (kV), or one of them: a wave owns 32 keys, a workgroup 32 W
 // consecutive ones, for G / splits query heads of the group.  Two stages of
 // query tiles (q rows, dout rows) and their lse and delta in LDS.
-template <int D, int W, bool kV, bool kK>
-__device__ __forceinline__ void kv_part(const AttnGradArgs& a, uint8_t* qb0, uint8_t* db0, uint8_t* qb1, uint8_t* db1,
-                                        float* lb0, float* eb0, float* lb1, float* eb1, int block, int wave, int lane) {
+template <int D, int W, int R, int S, bool kV, bool kK, typename X, typename Y, typename Z>
+__device__ __forceinline__ void kv_part(const AttnGradArgs& a, X qslot, Y dslot, Z zslot, int block, int wave, int lane) {
     using T = Tile<D>;
     constexpr int kBN = 32 * W;
     const int c = lane & 31, h = lane >> 5;
@@ -64,24 +63,28 @@ __device__ __forceinline__ void kv_part(const AttnGradArgs& a, uint8_t* qb0, uin
     if (st.len == 0) return;
     const int n0 = ((st.len + kBN - 1) / kBN - st.rank) * kBN;
     const int wkey = n0 + wave * 32;
-    const int first = n0 / 64, last = (st.len + 63) / 64;     // query tiles [first, last) of 64 rows
+    const int first = n0 / R, last = (st.len + R - 1) / R;    // query tiles [first, last) of R rows
     const int per_head = last - first, steps = per_head * G;
 
-    const TileCopy<D, W> qcopy(wave, lane, f.q_stride), dcopy(wave, lane, a.dout_stride);
-    auto issue = [&](uint8_t* qb, uint8_t* db, float* lb, float* eb, int step) {
+    const TileCopy<D, W, R> qcopy(wave, lane, f.q_stride), dcopy(wave, lane, a.dout_stride);
+    auto issue = [&](uint8_t* qb, uint8_t* db, float* zb, int step) {
+        step = min(step, steps - 1);
         const int head = head0 + step / per_head, t = first + step % per_head;
-        const int rows = min(64, st.len - t * 64);
-        const int64_t row = st.start + (int64_t)t * 64;
+        const int rows = min(R, st.len - t * R);
+        const int64_t row = st.start + (int64_t)t * R;
         qcopy(f.q + row * f.q_stride + (int64_t)head * D, f.q_stride, rows, qb, wave);
         dcopy(a.dout + row * a.dout_stride + (int64_t)head * D, a.dout_stride, rows, db, wave);
-        if (wave == 0) {
-            const int64_t at = (int64_t)head * f.total_T + row;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_rsrc(a.lse2 + at, rows * 4), (lds_ptr_t)lb, 4, lane * 4, 0, 0, 0);
-            if constexpr (kK)
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(row_rsrc(a.delta + at, rows * 4), (lds_ptr_t)eb, 4, lane * 4, 0, 0, 0);
-        }
+        // every wave brings its own copy of the rows' lse and delta (64 of each; those past the rows read as 0)
+        const int64_t at = (int64_t)head * f.total_T + row;
+        float* z = zb + wave * 128;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(row_rsrc(a.lse2 + at, rows * 4), (lds_ptr_t)z, 4, lane * 4, 0, 0, 0);
+        if constexpr (kK)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(row_rsrc(a.delta + at, rows * 4), (lds_ptr_t)(z + 64), 4, lane * 4, 0, 0, 0);
     };
-    issue(qb0, db0, lb0, eb0, 0);
+    constexpr int kPer = 2 * decltype(qcopy)::kDma + (kK ? 2 : 1);       // copies of a tile per wave
+    issue(qslot(IC<0>{}), dslot(IC<0>{}), zslot(IC<0>{}), 0);
+    if constexpr (S > 2) issue(qslot(IC<1>{}), dslot(IC<1>{}), zslot(IC<1>{}), 1);
+    if constexpr (S > 3) issue(qslot(IC<2>{}), dslot(IC<2>{}), zslot(IC<2>{}), 2);
 
     bf16x8 kf[D / 16], vf[D / 16];
     const bool exists = wkey + c < st.len;
@@ -148,21 +151,19 @@ __device__ __forceinline__ void kv_part(const AttnGradArgs& a, uint8_t* qb0, uin
             }
         }
     };
-    auto tile = [&](const uint8_t* qb, const uint8_t* db, const float* lb, const float* eb, int t) {
-        if (t * 64 + 31 >= wkey) rows32(qb, db, lb, eb, 0, t * 64);
-        if (t * 64 + 63 >= wkey) rows32(qb, db, lb, eb, 1, t * 64 + 32);
-    };
-    auto step = [&](const uint8_t* qb, const uint8_t* db, const float* lb, const float* eb, uint8_t* qn, uint8_t* dn,
-                    float* ln, float* en, int i) {
-        wait_vm<0>();
+    for_stages<S>(steps, [&](auto u, int i) {
+        constexpr int refill = (decltype(u)::value + S - 1) % S;
+        wait_vm<(S - 2) * kPer>();
         stage_barrier();
-        if (i + 1 < steps) issue(qn, dn, ln, en, i + 1);
-        if (wkey < st.len) tile(qb, db, lb, eb, first + i % per_head);
-    };
-    for (int i = 0; i < steps; i += 2) {
-        step(qb0, db0, lb0, eb0, qb1, db1, lb1, eb1, i);
-        if (i + 1 < steps) step(qb1, db1, lb1, eb1, qb0, db0, lb0, eb0, i + 1);
-    }
+        issue(qslot(IC<refill>{}), dslot(IC<refill>{}), zslot(IC<refill>{}), i + S - 1);
+        const int t = first + i % per_head;
+        const float* z = zslot(u) + wave * 128;
+        if (wkey >= st.len) return;
+#pragma unroll
+        for (int n = 0; n < R / 32; ++n)
+            if (t * R + n * 32 + 31 >= wkey) rows32(qslot(u), dslot(u), z, z + 64, n, t * R + n * 32);
+    });
+    wait_vm<0>();                                // no copy may outlive the workgroup
     if (a.splits == 1) {
         if constexpr (kK) store_transposed<D>(a.dk + krow * a.dk_stride + (int64_t)kvh * D, dk, f.scale, h, exists);
         if constexpr (kV) store_transposed<D>(a.dv + krow * a.dv_stride + (int64_t)kvh * D, dv, 1.f, h, exists);
@@ -182,13 +183,13 @@ __device__ __forceinline__ void kv_part(const AttnGradArgs& a, uint8_t* qb0, uin
     }
 }
 
-// Adds up the splits of dk and dv: a workgroup takes 32 rows of a sequence.
+// Adds up the splits of dk and dv: a workgroup takes 8 rows of a sequence.
 template <int D>
 __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(AttnGradArgs a) {
     const AttnArgs& f = a.f;
-    const SeqTile st = find_seq_tile(f.cu, f.N, f.total_T, blockIdx.x, 32);
+    const SeqTile st = find_seq_tile(f.cu, f.N, f.total_T, blockIdx.x, 8);
     if (st.len == 0) return;
-    const int row0 = (st.rank - 1) * 32, rows = min(32, st.len - row0);
+    const int row0 = (st.rank - 1) * 8, rows = min(8, st.len - row0);
     const int per_row = f.Hkv * D / 4;
     const int64_t one = f.total_T * f.Hkv * D;
     for (int i = threadIdx.x; i < rows * per_row; i += 256) {
@@ -210,9 +211,8 @@ __global__ __launch_bounds__(256) void attn_dkv_sum_kernel(AttnGradArgs a) {
 }
 
 // dq: a wave owns 32 query rows of one head, a workgroup 32 W consecutive ones.
-template <int D, int W>
-__device__ __forceinline__ void dq_part(const AttnGradArgs& a, uint8_t* kb0, uint8_t* vb0, uint8_t* kb1, uint8_t* vb1,
-                                        int block, int wave, int lane) {
+template <int D, int W, int R, int S, typename X, typename Y>
+__device__ __forceinline__ void dq_part(const AttnGradArgs& a, X kslot, Y vslot, int block, int wave, int lane) {
     using T = Tile<D>;
     constexpr int kBM = 32 * W;
     const int c = lane & 31, h = lane >> 5;
@@ -223,17 +223,20 @@ __device__ __forceinline__ void dq_part(const AttnGradArgs& a, uint8_t* kb0, uin
     if (st.len == 0) return;
     const int q0 = (st.rank - 1) * kBM;
     const int wrow = q0 + wave * 32;
-    const int tiles = (min(q0 + kBM, st.len) + 63) / 64;
+    const int tiles = (min(q0 + kBM, st.len) + R - 1) / R;
 
     const uint16_t* kp = f.k + st.start * f.k_stride + (int64_t)kvh * D;
     const uint16_t* vp = f.v + st.start * f.v_stride + (int64_t)kvh * D;
-    const TileCopy<D, W> kcopy(wave, lane, f.k_stride), vcopy(wave, lane, f.v_stride);
+    const TileCopy<D, W, R> kcopy(wave, lane, f.k_stride), vcopy(wave, lane, f.v_stride);
     auto issue = [&](uint8_t* kb, uint8_t* vb, int t) {
-        const int rows = min(64, st.len - t * 64);
-        kcopy(kp + (int64_t)t * 64 * f.k_stride, f.k_stride, rows, kb, wave);
-        vcopy(vp + (int64_t)t * 64 * f.v_stride, f.v_stride, rows, vb, wave);
+        t = min(t, tiles - 1);
+        const int rows = min(R, st.len - t * R);
+        kcopy(kp + (int64_t)t * R * f.k_stride, f.k_stride, rows, kb, wave);
+        vcopy(vp + (int64_t)t * R * f.v_stride, f.v_stride, rows, vb, wave);
     };
-    issue(kb0, vb0, 0);
+    issue(kslot(IC<0>{}), vslot(IC<0>{}), 0);
+    if constexpr (S > 2) issue(kslot(IC<1>{}), vslot(IC<1>{}), 1);
+    if constexpr (S > 3) issue(kslot(IC<2>{}), vslot(IC<2>{}), 2);
 
     bf16x8 qf[D / 16], df[D / 16];
     const bool exists = wrow + c < st.len;
@@ -255,8 +258,8 @@ __device__ __forceinline__ void dq_part(const AttnGradArgs& a, uint8_t* kb0, uin
 
     auto tile = [&](const uint8_t* kb, const uint8_t* vb, int t) {
 #pragma unroll
-        for (int n = 0; n < 2; ++n) {
-            const int k0 = t * 64 + n * 32;
+        for (int n = 0; n < R / 32; ++n) {
+            const int k0 = t * R + n * 32;
             if (k0 > wrow + 31) continue;
             f32x16 s, e;
 #pragma unroll
@@ -285,16 +288,14 @@ __device__ __forceinline__ void dq_part(const AttnGradArgs& a, uint8_t* kb0, uin
         }
     };
     const int last = min(wrow + 32, st.len) - 1;
-    auto step = [&](const uint8_t* kb, const uint8_t* vb, uint8_t* kn, uint8_t* vn, int t) {
-        wait_vm<0>();
+    for_stages<S>(tiles, [&](auto u, int t) {
+        constexpr int refill = (decltype(u)::value + S - 1) % S;
+        wait_vm<(S - 2) * 2 * decltype(kcopy)::kDma>();
         stage_barrier();
-        if (t + 1 < tiles) issue(kn, vn, t + 1);
-        if (t * 64 <= last && wrow < st.len) tile(kb, vb, t);
-    };
-    for (int t = 0; t < tiles; t += 2) {
-        step(kb0, vb0, kb1, vb1, t);
-        if (t + 1 < tiles) step(kb1, vb1, kb0, vb0, t + 1);
-    }
+        issue(kslot(IC<refill>{}), vslot(IC<refill>{}), t + S - 1);
+        if (t * R <= last && wrow < st.len) tile(kslot(u), vslot(u), t);
+    });
+    wait_vm<0>();
     store_transposed<D>(a.dq + row * a.dq_stride + (int64_t)head * D, dq, f.scale, h, exists);
 }
 
@@ -304,20 +305,26 @@ __device__ __forceinline__ void dq_part(const AttnGradArgs& a, uint8_t* kb0, uin
 // registers), and forming p once more for dv costs less than losing the second
 // wave (13 packed sequences of up to 1531 rows, 16 heads of 128: 216 -> 192 us;
 // for D = 64 both fit, and apart they take 1030 instead of 907 us at T = 8192).
-template <int D, int W, bool kApart>
+template <int D, int W, int R, int S, bool kApart>
 __global__ __launch_bounds__(64 * W, 2) void attn_grad_kernel(AttnGradArgs a, int kv_blocks) {
-    constexpr int kTileB = 64 * Tile<D>::kRowB;
-    __shared__ __attribute__((aligned(1024))) uint8_t x0[kTileB], y0[kTileB], x1[kTileB], y1[kTileB];
-    __shared__ __attribute__((aligned(1024))) float l0[64], e0[64], l1[64], e1[64];
+    constexpr int kTileB = R * Tile<D>::kRowB, kZ = 128 * W;
+    // a variable per slot: the compiler then knows which reads a copy in flight cannot touch
+    __shared__ __attribute__((aligned(1024))) uint8_t x0[kTileB], x1[kTileB], y0[kTileB], y1[kTileB];
+    __shared__ __attribute__((aligned(1024))) uint8_t x2[S > 2 ? kTileB : 16], y2[S > 2 ? kTileB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t x3[S > 3 ? kTileB : 16], y3[S > 3 ? kTileB : 16];
+    __shared__ __attribute__((aligned(1024))) float z0[kZ], z1[kZ], z2[S > 2 ? kZ : 4], z3[S > 3 ? kZ : 4];
+    auto x = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(x0, x1, x2, x3); };
+    auto y = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(y0, y1, y2, y3); };
+    auto z = [&](auto u) -> float* { return pick_slot<decltype(u)::value>(z0, z1, z2, z3); };
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     const int b = blockIdx.x;
     if (b < kv_blocks) {
-        kv_part<D, W, !kApart, true>(a, x0, y0, x1, y1, l0, e0, l1, e1, b, wave, lane);
+        kv_part<D, W, R, S, !kApart, true>(a, x, y, z, b, wave, lane);
     } else if (kApart && b < 2 * kv_blocks) {
-        kv_part<D, W, true, false>(a, x0, y0, x1, y1, l0, e0, l1, e1, b - kv_blocks, wave, lane);
+        kv_part<D, W, R, S, true, false>(a, x, y, z, b - kv_blocks, wave, lane);
     } else {
-        dq_part<D, W>(a, x0, y0, x1, y1, b - (kApart ? 2 : 1) * kv_blocks, wave, lane);
+        dq_part<D, W, R, S>(a, x, y, b - (kApart ? 2 : 1) * kv_blocks, wave, lane);
     }
 }
 
@@ -332,28 +339,30 @@ constexpr int kGW = 4;                           // waves per workgroup
 int attn_backward_splits(int Hq, int Hkv, int64_t total_T, int N) {
     const int G = Hq / Hkv;
     const int64_t blocks = (total_T / (32 * kGW) + 1) * Hkv;
+    // a walk of few tiles is shorter than the launch that adds the splits up
+    const int64_t tiles = (total_T / N + 63) / 64;
     for (int s = 1; s < G; ++s)
-        if (G % s == 0 && blocks * s >= 512) return s;
+        if (G % s == 0 && (blocks * s >= 512 || G / s * tiles <= 4)) return s;
     return G;
 }
 
-template <int D, bool kApart>
+template <int D, int R, int S, bool kApart>
 static hipError_t launch_bwd(const AttnGradArgs& a, hipStream_t s) {
     const AttnArgs& f = a.f;
     const int64_t rows = 32 * kGW, per_row = f.N == 1 ? (f.total_T + rows - 1) / rows : f.total_T / rows + f.N;
     const int64_t kv = per_row * f.Hkv * a.splits, all = kv * (kApart ? 2 : 1) + per_row * f.Hq;
-    const int64_t sums = f.total_T / 32 + f.N;
+    const int64_t sums = f.total_T / 8 + f.N;
     if (all >= ((int64_t)1 << 31) || sums >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
     const int heads = 64 / (D / 8);
     hipLaunchKernelGGL((attn_delta_kernel<D>), dim3((uint32_t)((f.total_T + 31) / 32), (f.Hq + heads - 1) / heads), dim3(256),
                        0, s, a);
-    hipLaunchKernelGGL((attn_grad_kernel<D, kGW, kApart>), dim3((uint32_t)all), dim3(64 * kGW), 0, s, a, (int)kv);
+    hipLaunchKernelGGL((attn_grad_kernel<D, kGW, R, S, kApart>), dim3((uint32_t)all), dim3(64 * kGW), 0, s, a, (int)kv);
     if (a.splits > 1) hipLaunchKernelGGL((attn_dkv_sum_kernel<D>), dim3((uint32_t)sums), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
 hipError_t launch_attn_backward(const AttnGradArgs& a, int D, hipStream_t s) {
-    return D == 64 ? launch_bwd<64, false>(a, s) : launch_bwd<128, true>(a, s);
+    return D == 64 ? launch_bwd<64, 64, 3, false>(a, s) : launch_bwd<128, 32, 3, true>(a, s);
 }
 
 }  // namespace lfm2sc

@@ -131,6 +131,31 @@ struct TileCopy {
     }
 };
 
+// A ring of S staged tiles: step(IC<u>, t) for t = 0 .. n - 1 with u = t % S.  The
+// step waits for tile t, meets the workgroup, refills slot (u + S - 1) % S with
+// tile min(t + S - 1, n - 1) (always, so that the number of copies in flight at
+// every wait is a constant) and computes from slot u.
+template <int u, typename T>
+__device__ __forceinline__ T* pick_slot(T* a, T* b, T* c, T* d) {
+    if constexpr (u == 0) return a;
+    else if constexpr (u == 1) return b;
+    else if constexpr (u == 2) return c;
+    else return d;
+}
+template <int S, typename F>
+__device__ __forceinline__ void for_stages(int n, F step) {
+    for (int t = 0; t < n; t += S) {
+        step(IC<0>{}, t);
+        if (t + 1 < n) step(IC<1>{}, t + 1);
+        if constexpr (S > 2) {
+            if (t + 2 < n) step(IC<2>{}, t + 2);
+        }
+        if constexpr (S > 3) {
+            if (t + 3 < n) step(IC<3>{}, t + 3);
+        }
+    }
+}
+
 // Row operand (B[k = value][n = row]) of row c: values 16 s + 8 h .. of a row in
 // global memory; zeros where the row does not exist.
 template <int D>

@@ -25,12 +25,17 @@ __device__ __forceinline__ int folded(int t, int blocks, int fold) {
     return (round & 1) && (round + 1) * fold <= blocks ? round * fold + fold - 1 - t % fold : t;
 }
 
-template <int D, int QB, int W, int kKT>
+template <int D, int QB, int W, int kKT, int S>
 __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a, int fold) {
     using T = Tile<D>;
     constexpr int kBM = 32 * QB * W, NB = kKT / 32;
     constexpr int kTileB = kKT * T::kRowB;
-    __shared__ __attribute__((aligned(1024))) uint8_t kbuf0[kTileB], kbuf1[kTileB], vbuf0[kTileB], vbuf1[kTileB];
+    // a variable per slot: the compiler then knows which reads a copy in flight cannot touch
+    __shared__ __attribute__((aligned(1024))) uint8_t k0[kTileB], k1[kTileB], v0[kTileB], v1[kTileB];
+    __shared__ __attribute__((aligned(1024))) uint8_t k2[S > 2 ? kTileB : 16], v2[S > 2 ? kTileB : 16];
+    __shared__ __attribute__((aligned(1024))) uint8_t k3[S > 3 ? kTileB : 16], v3[S > 3 ? kTileB : 16];
+    auto kslot = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(k0, k1, k2, k3); };
+    auto vslot = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(v0, v1, v2, v3); };
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
@@ -49,12 +54,15 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a, int fol
     const uint16_t* vp = a.v + st.start * a.v_stride + (int64_t)kvh * D;
     const TileCopy<D, W, kKT> kcopy(wave, lane, a.k_stride), vcopy(wave, lane, a.v_stride);
     auto issue = [&](uint8_t* kb, uint8_t* vb, int t) {
+        t = min(t, tiles - 1);
         const int rows = min(kKT, st.len - t * kKT);
         kcopy(kp + (int64_t)t * kKT * a.k_stride, a.k_stride, rows, kb, wave);
         vcopy(vp + (int64_t)t * kKT * a.v_stride, a.v_stride, rows, vb, wave);
     };
 
-    issue(kbuf0, vbuf0, 0);
+    issue(k0, v0, 0);
+    if constexpr (S > 2) issue(k1, v1, 1);
+    if constexpr (S > 3) issue(k2, v2, 2);
 
     // the wave's queries as B operands: row c of each block, values 16 s + 8 h ..
     bf16x8 qf[QB][D / 16];
@@ -147,16 +155,14 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a, int fol
     };
 
     const int last = min(wrow + 32 * QB, st.len) - 1;    // the wave's last row
-    auto step = [&](const uint8_t* kb, const uint8_t* vb, uint8_t* knext, uint8_t* vnext, int t) {
-        wait_vm<0>();
+    for_stages<S>(tiles, [&](auto u, int t) {
+        constexpr int refill = (decltype(u)::value + S - 1) % S;
+        wait_vm<(S - 2) * 2 * decltype(kcopy)::kDma>();
         stage_barrier();
-        if (t + 1 < tiles) issue(knext, vnext, t + 1);
-        if (t * kKT <= last && wrow < st.len) tile(kb, vb, t);
-    };
-    for (int t = 0; t < tiles; t += 2) {
-        step(kbuf0, vbuf0, kbuf1, vbuf1, t);
-        if (t + 1 < tiles) step(kbuf1, vbuf1, kbuf0, vbuf0, t + 1);
-    }
+        issue(kslot(IC<refill>{}), vslot(IC<refill>{}), t + S - 1);
+        if (t * kKT <= last && wrow < st.len) tile(kslot(u), vslot(u), t);
+    });
+    wait_vm<0>();                                // no copy may outlive the workgroup
 
 #pragma unroll
     for (int qb = 0; qb < QB; ++qb) {
@@ -168,7 +174,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a, int fol
     }
 }
 
-template <int D, int QB, int W, int KT>
+template <int D, int QB, int W, int KT, int S>
 static hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
     // sum ceil(len / rows) over the sequences is at most this
     const int64_t rows = 32 * QB * W, per_head = a.N == 1 ? (a.total_T + rows - 1) / rows : a.total_T / rows + a.N;
@@ -176,12 +182,12 @@ static hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
     if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
     constexpr int kResident = 256 * (D == 64 ? 4 : 3);           // workgroups
     const int fold = a.N == 1 && blocks <= kResident ? 256 / a.Hq : 0;
-    hipLaunchKernelGGL((attn_fwd_kernel<D, QB, W, KT>), dim3((uint32_t)blocks), dim3(64 * W), 0, s, a, fold);
+    hipLaunchKernelGGL((attn_fwd_kernel<D, QB, W, KT, S>), dim3((uint32_t)blocks), dim3(64 * W), 0, s, a, fold);
     return hipGetLastError();
 }
 
 hipError_t launch_attn_prefill(const AttnArgs& a, int D, hipStream_t s) {
-    return D == 64 ? launch_fwd<64, 1, 4, 64>(a, s) : launch_fwd<128, 1, 4, 32>(a, s);
+    return D == 64 ? launch_fwd<64, 1, 4, 64, 2>(a, s) : launch_fwd<128, 1, 4, 32, 3>(a, s);
 }
 
 }  // namespace lfm2sc
