@@ -8,7 +8,12 @@
 // Two passes over the score blocks, neither with atomics, so the gradients are
 // the same bits every time: one by key blocks (dk, dv stay in registers while
 // the group's heads and queries stream past), one by query blocks (dq stays,
-// keys stream).  Both form p again from q, k and lse.
+// keys stream).  Both form p again from q, k and lse: 7 products for the 5 that the
+// formulas need (8 where dk and dv go apart).  Per executed product the long case is
+// near what a library product reaches (T = 8192, 32 / 8 heads of 64: 889 us = 1.08
+// PFLOP/s executed, 0.77 of the formulas' five); D = 128 waits more (two waves per
+// SIMD, 37% of the cycles in the matrix unit).  dq summed with atomics would save
+// two products and the bits' order.
 #include "attn_common.hpp"
 #include "hybrid.hpp"
 
@@ -48,8 +53,8 @@ __global__ __launch_bounds__(256) void attn_delta_kernel(AttnGradArgs a) {
 }
 
 // dk (kK) and dv (kV), or one of them: a wave owns 32 keys, a workgroup 32 W
-// consecutive ones, for G / splits query heads of the group.  Two stages of
-// query tiles (q rows, dout rows) and their lse and delta in LDS.
+// consecutive ones, for G / splits query heads of the group.  S slots of R-row
+// query tiles (q rows, dout rows) and of their lse and delta in LDS.
 template <int D, int W, int R, int S, bool kV, bool kK, typename X, typename Y, typename Z>
 __device__ __forceinline__ void kv_part(const AttnGradArgs& a, X qslot, Y dslot, Z zslot, int block, int wave, int lane) {
     using T = Tile<D>;
@@ -361,8 +366,10 @@ static hipError_t launch_bwd(const AttnGradArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// R rows per staged tile and S slots.  D = 64: 64, 3 (gradients at T = 8192 889 us; 64, 2 1093; 32, 4 1150; 64, 4 as
+// 64, 3).  D = 128: 64, 2 (a training step of 13 x 1531 rows 258.5 us; 32, 3 262.5; 32, 4 267).
 hipError_t launch_attn_backward(const AttnGradArgs& a, int D, hipStream_t s) {
-    return D == 64 ? launch_bwd<64, 64, 3, false>(a, s) : launch_bwd<128, 32, 3, true>(a, s);
+    return D == 64 ? launch_bwd<64, 64, 3, false>(a, s) : launch_bwd<128, 64, 2, true>(a, s);
 }
 
 }  // namespace lfm2sc

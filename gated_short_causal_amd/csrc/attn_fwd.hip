@@ -2,18 +2,28 @@
 //
 // One pass over the keys with the running maximum m and sum l of each query
 // row's softmax.  A wave owns 32 QB query rows of one head; a workgroup's W
-// waves own consecutive rows and share the K and V tiles (64 keys) that are
-// copied to LDS ahead of use.  Scores are formed transposed, S^T = K Q^T, so
+// waves own consecutive rows and share the K and V tiles (kKT keys) that are
+// copied to LDS ahead of use, S slots of them.  Scores are formed transposed, S^T = K Q^T, so
 // that a lane holds 16 keys of one query per 32-key block: the row maximum and
 // sum are in-lane up to one exchange between the wave's halves, and
 // P^T = exp(S^T - m), rounded to bf16, is in place as the operand of
 // O^T += V^T P^T.  P never leaves the registers.
+//
+// What bounds it: long prompts run at the clock that the matrix and vector units
+// leave each other (1.9 GHz of 2.4): T = 8192, 32 / 8 heads of 64, 280 us = 980
+// TFLOP/s with the vector unit busy 76% and the matrix unit 50% of the cycles;
+// 16 / 2 heads of 128, 260-270 us = 1.03 PFLOP/s (a library product of 8192^3:
+// 1.24).  One sequence of up to ~2000 tokens has fewer workgroups than CUs or not
+// many more, and takes the time of its longest row block: about 0.9 us per 64 keys
+// (T = 1024: 16.6 us).  Measured and not kept: 64 rows per wave (75 us at 8 x 2048
+// against 67), 8 waves (70), 128-key tiles (68), separate code for tiles without
+// a mask (116 -> 162 registers: 336 us at 8192 against 304).
 #include "attn_common.hpp"
 #include "hybrid.hpp"
 
 namespace lfm2sc {
 
-constexpr float kLazy = 8.f;
+constexpr float kLazy = 8.f;      // how far (log2) a row's maximum may pass its reference m
 
 // A launch of one sequence whose workgroups are all resident at once: CU i gets
 // blocks i, i + 256, .. in falling order, so the CUs with the first of each

@@ -475,3 +475,66 @@ def test_another_stream():
         g.lfm2sc_attn_prefill(*late, args[3], 64, got[:, :512])
     side.synchronize()
     assert torch.equal(out[:, :512], got[:, :512])
+
+
+def test_example_runs_them_together():
+    from examples import hybrid_step
+    dev = torch.device(DEV)
+    torch.manual_seed(0)
+    for x in hybrid_step.train_step([70, 1, 130], dev).values():
+        assert torch.isfinite(x.float()).all()
+    s = hybrid_step.speculative_step(5, 3, 100, dev, vocab=300)
+    assert torch.isfinite(s["out"].float()).all()
+    for i, a in enumerate(s["accepted"].tolist()):
+        assert 0 <= a <= 3 and 0 <= s["next"][i] < 300
+        assert torch.equal(s["pool"][s["slots"][i].item()], s["tape"][i, a])
+
+
+_CHECK_SCRIPT = """
+import sys
+sys.path.insert(0, sys.argv[1])
+import torch
+import gated_short_causal_amd as g
+I32, BF, d = torch.int32, torch.bfloat16, "cuda"
+
+def status(call):
+    try:
+        call()
+        return 0
+    except g.Lfm2scError as e:
+        return e.status
+
+def ints(*v):
+    return torch.tensor(v, dtype=I32, device=d)
+
+x = torch.randn(20, 128, device=d).to(BF)
+out, lse = torch.empty_like(x), torch.empty(2, 20, device=d)
+def prompt(*cu):
+    return status(lambda: g.lfm2sc_attn_prefill(x, x, x, ints(*cu), 64, out, lse=lse))
+pool = torch.randn(8, 16, 2, 64, device=d).to(BF)
+def cached(pp, table, n):
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=d)
+    return status(lambda: g.lfm2sc_attn_cached(x[:1], pool, pool, ints(pp), 10, ints(table).reshape(1, 1), ints(n), 1, out[:1], ws))
+p, u, r = torch.rand(2, 50, device=d), torch.rand(1, 1, device=d), torch.empty(2, dtype=I32, device=d)
+def drafts(token, n):
+    ws = torch.empty(1 << 12, dtype=torch.uint8, device=d)
+    return status(lambda: g.lfm2sc_accept_drafts(p, ints(token).reshape(1, 1), u, u[0], r[:1], r[1:], ws, num_drafts=ints(n)))
+s = [prompt(0, 5, 20), prompt(0, 21), prompt(7, 3), cached(1, 2, 16), cached(8, 2, 16), cached(1, -1, 16), cached(1, 2, 17),
+     drafts(49, 1), drafts(50, 1), drafts(0, 2)]
+torch.cuda.synchronize()
+print("STATUS", s)
+"""
+
+
+def test_check_mode_reports_bad_device_data():
+    """LFM2SC_CHECK=1 (read once per process, hence a child) turns row offsets, pages, lengths, tokens and numbers of drafts
+    out of range into LFM2SC_ERR_PRECONDITION (6)."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _CHECK_SCRIPT, root], env=dict(os.environ, LFM2SC_CHECK="1"), capture_output=True,
+                       text=True, timeout=120)
+    assert r.returncode == 0, r.stderr[-2000:]
+    line = [x for x in r.stdout.splitlines() if x.startswith("STATUS")][0]
+    assert line == "STATUS [0, 6, 6, 0, 6, 6, 6, 0, 6, 6]", line
