@@ -29,16 +29,15 @@ def train_step(lens, dev):
     g.lfm2sc_prefill_ragged(conv_in, cu, w, y)
     g.lfm2sc_backward(conv_in, cu, w, dy, d_conv, dw, ws)
 
-    # q, k and v are columns of one projection's rows, their gradients columns of one buffer
-    qkv, do = rand(T, (HEADS + 2 * KV) * D, dev=dev), rand(T, HEADS * D, dev=dev)
-    split = [HEADS * D, KV * D, KV * D]
-    d_qkv, out, lse = torch.empty_like(qkv), torch.empty_like(do), torch.empty(HEADS, T, device=dev)
-    q, k, v = qkv.split(split, 1)
-    dq, dk, dv = d_qkv.split(split, 1)
+    # k and v are columns of one projection's rows, their gradients columns of one buffer
+    q, kv, do = rand(T, HEADS * D, dev=dev), rand(T, 2 * KV * D, dev=dev), rand(T, HEADS * D, dev=dev)
+    out, lse, dq, d_kv = torch.empty_like(q), torch.empty(HEADS, T, device=dev), torch.empty_like(q), torch.empty_like(kv)
+    k, v = kv.split(KV * D, 1)
+    dk, dv = d_kv.split(KV * D, 1)
     ws = torch.empty(g.lfm2sc_attn_backward_workspace_bytes(BF, D, HEADS, KV, T, N), dtype=torch.uint8, device=dev)
     g.lfm2sc_attn_prefill(q, k, v, cu, D, out, lse=lse)
     g.lfm2sc_attn_backward(q, k, v, cu, D, out, lse, do, dq, dk, dv, ws)
-    return {"y": y, "d_conv": d_conv, "dw": dw, "out": out, "lse": lse, "d_qkv": d_qkv}
+    return {"y": y, "d_conv": d_conv, "dw": dw, "out": out, "lse": lse, "dq": dq, "d_kv": d_kv}
 
 
 def speculative_step(seqs, drafts, prefix, dev, vocab=4096, page=16):
