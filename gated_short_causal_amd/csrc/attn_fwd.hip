@@ -15,7 +15,8 @@
 // 16 / 2 heads of 128, 260-270 us = 1.03 PFLOP/s (a library product of 8192^3:
 // 1.24).  One sequence of up to ~2000 tokens has fewer workgroups than CUs or not
 // many more, and takes the time of its longest row block: about 0.9 us per 64 keys
-// (T = 1024: 16.6 us).  Measured and not kept: 64 rows per wave (75 us at 8 x 2048
+// (T = 1024: 16.6 us; two wave groups that share its keys, joined in LDS: 15.9).
+// Measured and not kept: 64 rows per wave (75 us at 8 x 2048
 // against 67), 8 waves (70), 128-key tiles (68), separate code for tiles without
 // a mask (116 -> 162 registers: 336 us at 8192 against 304).
 #include "attn_common.hpp"
@@ -197,6 +198,8 @@ static hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_attn_prefill(const AttnArgs& a, int D, hipStream_t s) {
+    // keys per tile and slots: D = 64 leaves four workgroups per CU with two slots of 64 keys (8 x 2048: 56.3 us; 32, 3
+    // and 64, 3 60), D = 128 three with three slots of 32 (13 x 1531: 52.1 us; 32, 2 54.0; 32, 4 57.6; 64, 2 56.2)
     return D == 64 ? launch_fwd<64, 1, 4, 64, 2>(a, s) : launch_fwd<128, 1, 4, 32, 3>(a, s);
 }
 
