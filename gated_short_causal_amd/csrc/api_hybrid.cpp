@@ -13,6 +13,7 @@ using namespace lfm2sc;
 
 constexpr int64_t kMaxRowStride = (int64_t)1 << 22;   // 64 rows of a tile stay within 32-bit byte offsets
 constexpr int kMaxHeads = 1 << 14;
+constexpr int64_t kMaxKeys = (int64_t)1 << 30;        // a tile past a sequence's end still counts in an int
 
 int check_heads(const char* fn, int dtype, int D, int Hq, int Hkv) {
     if (dtype != LFM2SC_BF16) return fail(LFM2SC_ERR_UNSUPPORTED, "%s: only LFM2SC_BF16 is supported", fn);
@@ -39,8 +40,8 @@ int check_rows(const char* fn, const char* name, int64_t stride, int64_t min) {
 
 int check_tokens(const char* fn, int64_t total_T, int num_seqs) {
     if (num_seqs < 0) return fail(LFM2SC_ERR_BAD_SHAPE, "%s: num_seqs=%d is negative", fn, num_seqs);
-    if (total_T < 0 || total_T >= kMaxRows)
-        return fail(LFM2SC_ERR_BAD_SHAPE, "%s: total_T=%lld outside [0, 2^31)", fn, (long long)total_T);
+    if (total_T < 0 || total_T >= kMaxKeys)
+        return fail(LFM2SC_ERR_BAD_SHAPE, "%s: total_T=%lld outside [0, 2^30)", fn, (long long)total_T);
     return LFM2SC_OK;
 }
 
@@ -95,11 +96,12 @@ int check_cached_sizes(const char* fn, int N, int L, int Hq, int prefix_len, int
     if (N < 0 || L < 0) return fail(LFM2SC_ERR_BAD_SHAPE, "%s: num_seqs=%d or L=%d is negative", fn, N, L);
     if ((int64_t)N * L * Hq >= ((int64_t)1 << 28))
         return fail(LFM2SC_ERR_BAD_SHAPE, "%s: num_seqs * L * num_heads is 2^28 or more", fn);
-    if (prefix_len < 0) return fail(LFM2SC_ERR_BAD_SHAPE, "%s: prefix_len=%d is negative", fn, prefix_len);
+    if (prefix_len < 0 || prefix_len >= kMaxKeys)
+        return fail(LFM2SC_ERR_BAD_SHAPE, "%s: prefix_len=%d outside [0, 2^30)", fn, prefix_len);
     if (page_size < 1 || (page_size & (page_size - 1)) != 0)
         return fail(LFM2SC_ERR_BAD_SHAPE, "%s: page_size=%d is not a power of two", fn, page_size);
-    if (max_pages < 0 || (int64_t)max_pages * page_size >= kMaxRows)
-        return fail(LFM2SC_ERR_BAD_SHAPE, "%s: max_pages=%d of %d tokens outside [0, 2^31)", fn, max_pages, page_size);
+    if (max_pages < 0 || (int64_t)max_pages * page_size >= kMaxKeys)
+        return fail(LFM2SC_ERR_BAD_SHAPE, "%s: max_pages=%d of %d tokens outside [0, 2^30)", fn, max_pages, page_size);
     return LFM2SC_OK;
 }
 
@@ -141,7 +143,7 @@ int lfm2sc_attn_prefill(int dtype, int D, int num_heads, int num_kv_heads, const
 size_t lfm2sc_attn_backward_workspace_bytes(int dtype, int D, int num_heads, int num_kv_heads, int64_t total_T,
                                             int num_seqs) {
     if (dtype != LFM2SC_BF16 || (D != 64 && D != 128) || num_kv_heads < 1 || num_heads < num_kv_heads ||
-        num_heads % num_kv_heads != 0 || num_heads > kMaxHeads || total_T <= 0 || total_T >= kMaxRows || num_seqs <= 0)
+        num_heads % num_kv_heads != 0 || num_heads > kMaxHeads || total_T <= 0 || total_T >= kMaxKeys || num_seqs <= 0)
         return 0;
     const size_t rows = 2 * round_up((size_t)num_heads * (size_t)total_T * 4);
     const int splits = attn_backward_splits(num_heads, num_kv_heads, total_T, num_seqs);
@@ -206,8 +208,8 @@ size_t lfm2sc_attn_cached_workspace_bytes(int dtype, int D, int num_heads, int n
                                           int prefix_len, int max_pages, int page_size) {
     if (dtype != LFM2SC_BF16 || (D != 64 && D != 128) || num_kv_heads < 1 || num_heads < num_kv_heads ||
         num_heads % num_kv_heads != 0 || num_heads > kMaxHeads || num_seqs <= 0 || L <= 0 ||
-        (int64_t)num_seqs * L * num_heads >= ((int64_t)1 << 28) || prefix_len < 0 || page_size < 1 ||
-        (page_size & (page_size - 1)) != 0 || max_pages < 0 || (int64_t)max_pages * page_size >= kMaxRows)
+        (int64_t)num_seqs * L * num_heads >= ((int64_t)1 << 28) || prefix_len < 0 || prefix_len >= kMaxKeys ||
+        page_size < 1 || (page_size & (page_size - 1)) != 0 || max_pages < 0 || (int64_t)max_pages * page_size >= kMaxKeys)
         return 0;
     return cached_bytes(D, num_heads, num_kv_heads, num_seqs, L, prefix_len, max_pages * page_size);
 }

@@ -30,7 +30,8 @@
  *    [h*D, (h+1)*D)); strides are multiples of 8 elements, at least heads * D,
  *    below 2^22; pointers are 16-byte aligned (lse and int32 arrays: 4-byte), so
  *    q, k and v may be column ranges of one projection's rows.
- *  - scale multiplies q.k; finite and > 0.
+ *  - scale multiplies q.k; finite and > 0.  total_T, prefix_len and max_pages *
+ *    page_size are below 2^30.
  *  - An infinity or NaN in k or v of a token reaches the rows that see the token,
  *    and may reach earlier rows of the same sequence within 127 tokens of it
  *    (their probability of it is 0, but 0 * infinity is not).  It reaches no

@@ -38,7 +38,7 @@ COMMON = [
     (dict(dtype=1), UNSUP), (dict(dtype=5), UNSUP), (dict(D=96), UNSUP), (dict(D=0), UNSUP), (dict(Hkv=0), SHAPE),
     (dict(Hq=6, Hkv=4), SHAPE), (dict(Hq=1, Hkv=2), SHAPE), (dict(Hq=-2), SHAPE),
     (dict(scale=0.0), SHAPE), (dict(scale=-1.0), SHAPE), (dict(scale=math.inf), SHAPE), (dict(scale=math.nan), SHAPE),
-    (dict(T=-1), SHAPE), (dict(T=1 << 31), SHAPE), (dict(N=-1), SHAPE), (dict(T=(1 << 31) - 1, Hq=1 << 12), SHAPE),
+    (dict(T=-1), SHAPE), (dict(T=1 << 31), SHAPE), (dict(T=1 << 30), SHAPE), (dict(N=-1), SHAPE), (dict(T=(1 << 31) - 1, Hq=1 << 12), SHAPE),
     (dict(qs=504), SHAPE), (dict(qs=516), ALIGN), (dict(ks=120), SHAPE), (dict(vs=130), ALIGN), (dict(os=511), SHAPE),
     (dict(ks=1 << 22), SHAPE), (dict(q=None), NULLP), (dict(k=None), NULLP), (dict(v=None), NULLP), (dict(cu=None), NULLP),
     (dict(out=None), NULLP), (dict(q=MIS), ALIGN), (dict(k=P + 8), ALIGN), (dict(v=MIS), ALIGN), (dict(out=MIS), ALIGN),
@@ -97,7 +97,8 @@ def _cached(L, **kw):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(dtype=1), UNSUP), (dict(D=32), UNSUP), (dict(Hq=7), SHAPE), (dict(Hkv=0), SHAPE), (dict(scale=math.nan), SHAPE),
-    (dict(N=-1), SHAPE), (dict(Lb=-1), SHAPE), (dict(N=1 << 20, Lb=1 << 10), SHAPE), (dict(plen=-1), SHAPE),
+    (dict(N=-1), SHAPE), (dict(Lb=-1), SHAPE), (dict(N=1 << 20, Lb=1 << 10), SHAPE), (dict(plen=-1), SHAPE), (dict(plen=1 << 30), SHAPE),
+    (dict(most=1 << 26), SHAPE),
     (dict(page=0), SHAPE), (dict(page=24), SHAPE), (dict(page=-16), SHAPE), (dict(most=-1), SHAPE),
     (dict(most=1 << 27), SHAPE), (dict(pages=0), SHAPE), (dict(pages=1 << 27), SHAPE),
     (dict(qs=504), SHAPE), (dict(qs=516), ALIGN), (dict(kvs=64), SHAPE), (dict(kvs=132), ALIGN), (dict(os=256), SHAPE),
