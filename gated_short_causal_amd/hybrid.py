@@ -37,7 +37,8 @@ def _refuse(t, name, dev, dtype, what):
 
 
 def _mat(t, name, dev, dtype, rows, cols):
-    """Row stride of a matrix of at least rows x cols with unit column stride."""
+    """Row stride of a matrix of at least rows x cols with unit column stride.  Where the call addresses one row at most,
+    a stride below its width means nothing and the width stands in; else it goes to the library, which refuses it."""
     if t.dtype is dtype and t.get_device() == dev:
         shape = t.shape
         if len(shape) != 2:
@@ -45,7 +46,7 @@ def _mat(t, name, dev, dtype, rows, cols):
         r, c = shape
         s, unit = t.stride()
         if r >= rows and c >= cols and (unit == 1 or c <= 1):
-            return s
+            return s if s >= cols or rows > 1 else cols
     _refuse(t, name, dev, dtype, f"a matrix of at least [{rows}, {cols}] with unit column stride")
 
 
@@ -190,9 +191,9 @@ def lfm2sc_accept_drafts(target_probs, draft_tokens, u_accept, u_sample, accept_
     N, L = draft_tokens.shape
     V = target_probs.shape[-1]
     ts = _mat(target_probs, "target_probs", dev, dtype, N * (L + 1), V)
-    ds = 0 if draft_probs is None else _mat(draft_probs, "draft_probs", dev, dtype, N * L, V)
+    ds = V if draft_probs is None else _mat(draft_probs, "draft_probs", dev, dtype, N * L, V)
     rc = _lib.hybrid_lib().lfm2sc_accept_drafts(
-        _dtype_code(target_probs), V, N, L, target_probs.data_ptr(), ts if ts > V else V, _ptr(draft_probs), ds if ds > V else V,
+        _dtype_code(target_probs), V, N, L, target_probs.data_ptr(), ts, _ptr(draft_probs), ds,
         _vec(draft_tokens, "draft_tokens", dev, _I32, 0), _vec(num_drafts, "num_drafts", dev, _I32, N),
         _needed(u_accept, "u_accept", dev, _F32, N * L), _needed(u_sample, "u_sample", dev, _F32, N),
         _needed(accept_len, "accept_len", dev, _I32, N), _vec(keep_len, "keep_len", dev, _I32, N),
