@@ -261,6 +261,7 @@ __device__ __forceinline__ void own_part(const CachedArgs& a, uint8_t* buf0, uin
             if constexpr (more) {
                 rows = pool_row(a, next, key_of(t + W));
                 next = page_of(min(t + 2 * W, t1 - 1));
+                lds_reads_done();                // of this K tile
                 copy_paged<D, kN>(kp, a.kv_stride, rows, kb, 0, lane);
             }
         };
@@ -272,7 +273,10 @@ __device__ __forceinline__ void own_part(const CachedArgs& a, uint8_t* buf0, uin
         const bool shared = kDirect && t < pt;
         attend<D, KT>(r, qf, kb, vb, lo, cs, shared ? t * KT + KT > prefix : k0 + KT - 1 > len - a.L,
                       shared ? prefix - 1 - t * KT : last - k0, h, after_k, before_v);
-        if constexpr (more) copy_paged<D, kN>(vp, a.kv_stride, rows, vb, 0, lane);
+        if constexpr (more) {
+            lds_reads_done();                    // of this V tile
+            copy_paged<D, kN>(vp, a.kv_stride, rows, vb, 0, lane);
+        }
     };
     if (mine < t1) {
         int t = mine;

@@ -106,6 +106,16 @@ __device__ __forceinline__ bf16x8 lds_transposed(const uint8_t* tile, uint32_t o
     return __builtin_bit_cast(bf16x8, r);
 }
 
+// The wave's LDS reads have returned.  A copy to LDS is not ordered behind reads
+// issued before it, neither by the compiler nor by the hardware: a wave that
+// refills a tile which it has just read waits here first.  (Slots shared by a
+// workgroup are refilled behind a barrier, before which every read was consumed.)
+__device__ __forceinline__ void lds_reads_done() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((63 & 15) | (7 << 4) | (0 << 8) | ((63 >> 4) << 14));   // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+}
+
 // Copies of R-row tiles (row r at byte (r * stride) * 2 from the tile's first
 // row) to LDS, kDma KiB per wave; rows at or beyond the given count read as
 // zeros (the buffer's range check).
