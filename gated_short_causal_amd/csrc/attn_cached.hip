@@ -239,6 +239,8 @@ __device__ __forceinline__ void own_part(const CachedArgs& a, uint8_t* buf0, uin
     // The wave's next K tile is copied as soon as the scores of this one are formed, the next V tile after the
     // products with this one, and the page numbers a tile before that; so its waits leave the copies issued later in
     // flight.  Order of its vector memory operations: pages(t + 1), K(t), V(t), [pages(t + 2), K(t + 1)], V(t + 1), ..
+    // Each wait leaves exactly the copies of one tile in flight, so it holds however many loads the compiler makes of
+    // the page numbers; the one before V therefore waits for pages(t + 2) too.
     constexpr int kN = kTileB / 1024;
     const uint16_t* kp = a.k + (int64_t)kvh * D;
     const uint16_t* vp = a.v + (int64_t)kvh * D;
@@ -266,7 +268,7 @@ __device__ __forceinline__ void own_part(const CachedArgs& a, uint8_t* buf0, uin
             }
         };
         auto before_v = [&] {
-            wait_vm<more ? kN + 1 : 0>();
+            wait_vm<more ? kN : 0>();
             asm volatile("" ::: "memory");
         };
         const int k0 = (t - pt) * KT;            // first own key of the tile; negative: a tile of the prefix

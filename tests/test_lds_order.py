@@ -2,7 +2,9 @@
 
 A copy from global memory into LDS is not ordered behind a wave's earlier LDS reads: an instruction has to wait for them
 (lgkmcnt).  The check follows every path of a kernel and carries how many LDS operations came after the newest read of a
-staged tile, until a wait covers that read.
+staged tile, until a wait covers that read.  The other way round, a wave waits for a staged tile by the number of vector
+memory operations that may still be in flight (vmcnt): those have to be copies, whose number the source fixes, and no
+loads, whose number the compiler chooses.
 """
 import os
 import re
@@ -17,6 +19,8 @@ READ = re.compile(r"ds_read_(b128|b64)")                   # tiles are read 16 b
 QUEUED = re.compile(r"ds_|s_load|s_buffer_load")           # what lgkmcnt counts
 COPY = re.compile(r"global_load_lds|buffer_load\S*\s.*\blds\b")
 BARRIER = re.compile(r"s_barrier")
+VMEM = re.compile(r"global_(load|store)|buffer_(load|store)|flat_")
+VMWAIT = re.compile(r"s_waitcnt\b.*vmcnt\((\d+)\)")
 WAIT = re.compile(r"s_waitcnt\b.*lgkmcnt\((\d+)\)")
 
 
@@ -58,27 +62,39 @@ def _step(newer, instruction):
     return None if wait and int(wait.group(1)) <= newer else newer
 
 
-def _unwaited(graph, what):
-    """The instructions matching `what` that some path reaches with a tile read in flight."""
-    state, work = {"entry": None}, ["entry"]
+def _flow(graph, start, step):
+    """The least state (None: above all) in which some path reaches each instruction: (label, instruction, state)."""
+    state, work = {"entry": start}, ["entry"]
     while work:
         here = work.pop()
-        newer = state[here]
+        now = state[here]
         for i in graph[here][0]:
-            newer = _step(newer, i)
+            now = step(now, i)
         for to in graph[here][1]:
             old = state.get(to, "new")
-            joined = newer if old == "new" else min((x for x in (old, newer) if x is not None), default=None)
+            joined = now if old == "new" else min((x for x in (old, now) if x is not None), default=None)
             if joined != old:
                 state[to] = joined
                 work.append(to)
-    bad = []
-    for here, newer in state.items():
+    out = []
+    for here, now in state.items():
         for i in graph[here][0]:
-            if newer is not None and what.match(i):
-                bad.append((here, i))
-            newer = _step(newer, i)
-    return bad
+            out.append((here, i, now))
+            now = step(now, i)
+    return out
+
+
+def _unwaited(graph, what):
+    """The instructions matching `what` that some path reaches with a tile read in flight."""
+    return [(here, i) for here, i, newer in _flow(graph, None, _step) if newer is not None and what.match(i)]
+
+
+def _counts_a_load(graph, least):
+    """The waits that leave `least` or more operations in flight which on some path are not all copies."""
+    def step(run, i):                                # copies since the last other vector memory operation, at most 64
+        return min(run + 1, 64) if COPY.match(i) else 0 if VMEM.match(i) else run
+    return [(here, i) for here, i, run in _flow(graph, 0, step)
+            for n in VMWAIT.findall(i) if int(n) >= least and int(n) > run]
 
 
 @pytest.fixture(scope="module")
@@ -131,6 +147,19 @@ _Zthree:
     assert [len(_unwaited(k[n], COPY)) for n in ("_Zone", "_Ztwo", "_Zthree")] == [1, 0, 1]
 
 
+def test_the_check_sees_a_counted_load():
+    asm = """_Zone:
+ global_load_dword v0, v[1:2], off
+ global_load_lds_dwordx4 v[7:8], off
+ global_load_lds_dwordx4 v[7:8], off
+ s_waitcnt vmcnt(2)
+ s_waitcnt vmcnt(3) lgkmcnt(0)
+ s_endpgm
+.Lfunc_end0:
+"""
+    assert _counts_a_load(_kernels(asm)["_Zone"], 2) == [("entry", "s_waitcnt vmcnt(3) lgkmcnt(0)")]
+
+
 def _named(kernels, part):
     hits = {n: g for n, g in kernels.items() if part in n}
     assert hits, part
@@ -149,3 +178,10 @@ def test_barriers_wait_for_the_reads_of_the_tile(kernels):
     assert {p for p in ("attn_fwd", "attn_grad", "attn_cached") for n in kernels if p in n} == {"attn_fwd", "attn_grad", "attn_cached"}
     for name, graph in kernels.items():
         assert not _unwaited(graph, BARRIER), name
+
+
+@pytest.mark.parametrize("part", ["attn_cached_direct_kernel", "attn_cached_kernel"])
+def test_waits_for_a_tile_count_copies_only(kernels, part):
+    """The smallest tile is 4 copies: waits that leave 4 or more operations in flight are the kernels' own."""
+    for name, graph in _named(kernels, part).items():
+        assert not _counts_a_load(graph, 4), name
