@@ -243,7 +243,7 @@ int lfm2sc_attn_cached(int dtype, int D, int num_heads, int num_kv_heads, const 
     hipStream_t s = static_cast<hipStream_t>(stream);
     const RangeCheck ranges[] = {
         {prefix_pages, prefix_len > 0 ? ((int64_t)prefix_len + page_size - 1) / page_size : 0, 0, (int64_t)num_pages - 1},
-        {page_table, (int64_t)num_seqs * max_pages, 0, (int64_t)num_pages - 1},
+        {page_table, (int64_t)num_seqs * max_pages, 0, (int64_t)num_pages - 1, suffix_len, max_pages, page_size},
         {suffix_len, num_seqs, 0, (int64_t)max_pages * page_size}};
     const char* const names[] = {"a prefix page", "a page of page_table", "a suffix length"};
     TRY(check_ranges(fn, s, ranges, names, 3));
@@ -302,7 +302,7 @@ int lfm2sc_accept_drafts(int dtype, int V, int num_seqs, int L, const void* targ
     TRY(check_ptr(fn, "next_token", next_token, 4));
     TRY(check_workspace(fn, workspace, workspace_bytes, lfm2sc_accept_drafts_workspace_bytes(num_seqs, L, V), 8));
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const RangeCheck ranges[] = {{L > 0 ? draft_tokens : nullptr, (int64_t)num_seqs * L, 0, (int64_t)V - 1},
+    const RangeCheck ranges[] = {{L > 0 ? draft_tokens : nullptr, (int64_t)num_seqs * L, 0, (int64_t)V - 1, num_drafts, L},
                                  {num_drafts, num_seqs, 0, L}};
     const char* const names[] = {"a draft token", "a number of drafts"};
     TRY(check_ranges(fn, s, ranges, names, 2));

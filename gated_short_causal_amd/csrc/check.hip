@@ -7,6 +7,7 @@
 // debugging only.  The result travels through one device flag per process,
 // so a process-wide lock keeps each call's reset, checks and read-back
 // together: calls from several host threads take turns.
+#include <algorithm>
 #include <mutex>
 
 #include "common.hpp"
@@ -48,9 +49,11 @@ __global__ void check_accept_kernel(const int32_t* __restrict__ acc, int N, int 
     if (acc[i] < 0 || acc[i] > L) atomicOr(&g_check_flags, (int)kBadAccept);
 }
 
-__global__ void check_range_kernel(const int32_t* __restrict__ v, int64_t n, int64_t lo, int64_t hi, int flag) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i < n && (v[i] < lo || v[i] > hi)) atomicOr(&g_check_flags, flag);
+__global__ void check_range_kernel(RangeCheck c, int flag) {
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < c.n; i += (int64_t)gridDim.x * blockDim.x) {
+        if (c.len != nullptr && i % c.row * c.per >= c.len[i / c.row]) continue;
+        if (c.v[i] < c.lo || c.v[i] > c.hi) atomicOr(&g_check_flags, flag);
+    }
 }
 
 // The arrays' entries that leave their ranges, as bits 0, 1, .. by array.
@@ -60,8 +63,8 @@ int check_device_ranges(hipStream_t s, const RangeCheck* checks, int count, hipE
     for (int k = 0; k < count; ++k) {
         const RangeCheck& c = checks[k];
         if (c.v != nullptr && c.n > 0)
-            hipLaunchKernelGGL(check_range_kernel, dim3((uint32_t)((c.n + 255) / 256)), dim3(256), 0, s, c.v, c.n, c.lo,
-                               c.hi, 1 << k);
+            hipLaunchKernelGGL(check_range_kernel, dim3((uint32_t)std::min<int64_t>((c.n + 255) / 256, 65536)), dim3(256), 0, s,
+                               c, 1 << k);
     }
     int flags = 0;
     hipError_t e = hipGetLastError();

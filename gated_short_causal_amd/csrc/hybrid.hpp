@@ -69,10 +69,14 @@ struct DraftArgs {
 constexpr int kDraftChunk = 4096;                // tokens per chunk of the split form
 int draft_chunks(int V);
 
-// Host check of int32 device data (check.hip): n entries within [lo, hi].
+// Host check of int32 device data (check.hip): n entries within [lo, hi].  With
+// `len`, the entries are runs of `row`, of which run i uses the first
+// ceil(len[i] / per); the others may hold anything.
 struct RangeCheck {
     const int32_t* v;
     int64_t n, lo, hi;
+    const int32_t* len = nullptr;
+    int64_t row = 1, per = 1;
 };
 int check_device_ranges(hipStream_t s, const RangeCheck* checks, int count, hipError_t* err);
 

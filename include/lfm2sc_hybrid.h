@@ -107,7 +107,8 @@ size_t lfm2sc_attn_cached_workspace_bytes(int dtype, int D, int num_heads, int n
  *              before the call.
  * prefix_pages [ceil(prefix_len / page_size)] int32, prefix_len >= 0: the shared
  *              keys, seen by every row.  May be NULL when prefix_len is 0.
- * page_table   [num_seqs][max_pages] int32: each sequence's own pages.
+ * page_table   [num_seqs][max_pages] int32: each sequence's own pages.  Entries past
+ *              ceil(suffix_len[i] / page_size) are not used and may hold anything.
  * suffix_len   [num_seqs] int32: its own keys, the L new ones included; clamped to
  *              [0, max_pages * page_size].  Row i*L+s sees the prefix and own keys
  *              0 .. suffix_len[i]-L+s.  A row that sees no key gets zeros.
@@ -142,7 +143,8 @@ size_t lfm2sc_accept_drafts_workspace_bytes(int num_seqs, int L, int V);
  * draft_probs  [num_seqs*L][draft_stride] or NULL (deterministic drafts: the
  *              draft's own probability counts as 1).
  * draft_tokens [num_seqs][L] int32; one outside [0, V) is never accepted.
- * num_drafts   [num_seqs] int32 or NULL (= L for all), clamped to [0, L].
+ * num_drafts   [num_seqs] int32 or NULL (= L for all), clamped to [0, L].  Draft
+ *              tokens and numbers past it are not used and may hold anything.
  * u_accept     [num_seqs][L] fp32 and u_sample [num_seqs] fp32: uniform numbers in
  *              [0, 1) from the caller.
  * accept_len   [num_seqs] int32: a, the number of leading drafts s with
