@@ -6,7 +6,8 @@
 // fp64.  With a drafts accepted, the next token is drawn from
 //   r = p_a                         every draft accepted
 //   r = max(p_a - q_a, 0)           else (q_a: 1 at the draft's token when no
-//                                   draft probabilities are given)
+//                                   draft probabilities are given; in r, NaN and
+//                                   negative entries of both rows count as 0)
 //   r = p_a                         where that leaves nothing
 // as the lowest index whose running sum of r exceeds u sum r.  Sums and
 // differences are fp64 throughout: the differences are exact up to the last
@@ -98,9 +99,9 @@ __device__ __forceinline__ Draw<E> accept(const DraftArgs<E>& a, int n, int lane
 
 // r of 8 consecutive tokens from index i, of which x and y (kRows: there are
 // draft rows) are the target's and the draft's probabilities: max(x - y, 0),
-// without draft rows x outside the hole; 0 for the first `skip` (kEnd).  Compared
-// in fp32, which is exact, so that a NaN or negative entry counts as nothing; the
-// difference is fp64.
+// without draft rows x outside the hole; 0 for the first `skip` (kEnd).  A NaN or
+// negative y is 0 from the start (a median drops a NaN); the difference is fp64,
+// its sign is exact, and a NaN of it (x, or both infinite) counts as nothing.
 template <bool kRows, bool kEnd, typename E>
 __device__ __forceinline__ void weights(const Raw8<E>& xr, const Raw8<E>& yr, int i, int hole, int skip, double* r) {
     float x[8], y[8];
@@ -108,10 +109,14 @@ __device__ __forceinline__ void weights(const Raw8<E>& xr, const Raw8<E>& yr, in
     if constexpr (kRows) to_f32(yr, y);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        bool some = kRows ? x[j] > y[j] : x[j] > 0.f && i + j != hole;
-        if constexpr (kEnd) some = some && j >= skip;
-        r[j] = (double)(some ? x[j] : 0.f);
-        if constexpr (kRows) r[j] -= (double)(some ? y[j] : 0.f);
+        if constexpr (kRows) {
+            if constexpr (kEnd) x[j] = j >= skip ? x[j] : 0.f;
+            r[j] = fmax((double)x[j] - (double)__builtin_amdgcn_fmed3f(y[j], 0.f, __builtin_inff()), 0.);
+        } else {
+            bool some = x[j] > 0.f && i + j != hole;
+            if constexpr (kEnd) some = some && j >= skip;
+            r[j] = (double)(some ? x[j] : 0.f);
+        }
     }
 }
 __device__ __forceinline__ double sum8(const double* r) {

@@ -156,7 +156,9 @@ size_t lfm2sc_accept_drafts_workspace_bytes(int num_seqs, int L, int V);
  *              accepted, else max(p_a - q_a, 0) (p_a without the draft's token
  *              when draft_probs is NULL), else p_a where that is all zero: the
  *              lowest j with r_0 + .. + r_j > u_sample * sum r.  Sums are fp64; rows
- *              need not add up to 1.  NaN and negative entries count as 0.  For
+ *              need not add up to 1.  In r, NaN and negative entries of p_a and q_a
+ *              count as 0 (accept_len's comparison takes them as they are: a NaN
+ *              is never accepted).  For
  *              u_sample outside [0, 1) the last j with r_j > 0 (or, below 0, the
  *              first); -1 when the row has no positive entry.
  * 0 <= L <= 64, V >= 1; strides >= V, rows need only be aligned to an element.

@@ -102,6 +102,11 @@ def cached(q, k_pages, v_pages, prefix_pages, prefix_len, page_table, suffix_len
     return out, spread
 
 
+def _weights(row):
+    """A row's entries as weights: NaN and negative ones count as 0."""
+    return np.nan_to_num(row, nan=0.0, posinf=np.inf, neginf=0.0).clip(min=0.0)
+
+
 def accept_drafts(target, tokens, u_accept, u_sample, draft=None, num_drafts=None):
     """(accept_len, next_token) of each sequence."""
     target, draft, tokens = f64(target), f64(draft), np.asarray(tokens)
@@ -119,12 +124,12 @@ def accept_drafts(target, tokens, u_accept, u_sample, draft=None, num_drafts=Non
             if not float(u_accept[n, a]) * q < p:
                 break
             a += 1
-        p = np.nan_to_num(target[n * (L + 1) + a], nan=0.0, posinf=np.inf, neginf=0.0).clip(min=0.0)
+        p = _weights(target[n * (L + 1) + a])
         r = p
         if a < drafts:
             if draft is not None:
                 with np.errstate(invalid="ignore"):
-                    r = target[n * (L + 1) + a] - draft[n * L + a]
+                    r = p - _weights(draft[n * L + a])
                 r = np.where(r > 0, r, 0.0)
             else:
                 r = p.copy()
