@@ -50,19 +50,21 @@ def _mat(t, name, dev, dtype, rows, cols):
     _refuse(t, name, dev, dtype, f"a matrix of at least [{rows}, {cols}] with unit column stride")
 
 
-def _vec(t, name, dev, dtype, numel):
-    """Address of a contiguous tensor of at least numel entries; None for None."""
+def _vec(t, name, dev, dtype, numel, width=None):
+    """Address of a contiguous tensor of at least numel entries, a matrix in rows of `width`; None for None."""
     if t is None:
         return None
     if t.dtype is dtype and t.get_device() == dev and t.numel() >= numel and t.is_contiguous():
-        return t.data_ptr()
+        if width is None or t.dim() != 2 or t.shape[1] == width:
+            return t.data_ptr()
+        _refuse(t, name, dev, dtype, f"in rows of {width} entries")
     _refuse(t, name, dev, dtype, f"contiguous with at least {numel} entries")
 
 
-def _needed(t, name, dev, dtype, numel):
+def _needed(t, name, dev, dtype, numel, width=None):
     if t is None:
         raise ValueError(f"{name} is required")
-    return _vec(t, name, dev, dtype, numel)
+    return _vec(t, name, dev, dtype, numel, width)
 
 
 def _heads(width, D, name):
@@ -91,7 +93,7 @@ def _prompt(q, k, v, cu_seqlens, D, out, lse, scale):
     return dev, (_dtype_code(q), D, Hq, Hkv, q.data_ptr(), _mat(q, "q", dev, dtype, T, Hq * D),
                  k.data_ptr(), _mat(k, "k", dev, dtype, T, Hkv * D), v.data_ptr(), _mat(v, "v", dev, dtype, T, Hkv * D),
                  T, cu, cu_seqlens.numel() - 1, D ** -0.5 if scale is None else scale,
-                 out.data_ptr(), _mat(out, "out", dev, dtype, T, Hq * D)), _vec(lse, "lse", dev, _F32, Hq * T)
+                 out.data_ptr(), _mat(out, "out", dev, dtype, T, Hq * D)), _vec(lse, "lse", dev, _F32, Hq * T, T)
 
 
 def lfm2sc_attn_prefill(q, k, v, cu_seqlens, D, out, lse=None, scale=None):
@@ -195,7 +197,7 @@ def lfm2sc_accept_drafts(target_probs, draft_tokens, u_accept, u_sample, accept_
     rc = _lib.hybrid_lib().lfm2sc_accept_drafts(
         _dtype_code(target_probs), V, N, L, target_probs.data_ptr(), ts, _ptr(draft_probs), ds,
         _vec(draft_tokens, "draft_tokens", dev, _I32, 0), _vec(num_drafts, "num_drafts", dev, _I32, N),
-        _needed(u_accept, "u_accept", dev, _F32, N * L), _needed(u_sample, "u_sample", dev, _F32, N),
+        _needed(u_accept, "u_accept", dev, _F32, N * L, L), _needed(u_sample, "u_sample", dev, _F32, N),
         _needed(accept_len, "accept_len", dev, _I32, N), _vec(keep_len, "keep_len", dev, _I32, N),
         _needed(next_token, "next_token", dev, _I32, N), *_workspace(workspace, dev), binding._stream(target_probs.device))
     if rc:

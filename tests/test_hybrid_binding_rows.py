@@ -74,3 +74,29 @@ def test_true_strides_reach_the_library(lib):
     a.update(target_probs=torch.zeros(9, 16)[:, :11], draft_probs=torch.zeros(6, 13)[:, :11])
     hybrid.lfm2sc_accept_drafts(**a)
     assert lib.calls[0][1][5] == 16 and lib.calls[0][1][7] == 13
+
+
+def _prompt(T=10, D=64, Hq=4, Hkv=2, **change):
+    return {**dict(q=torch.zeros(T, Hq * D, dtype=BF), k=torch.zeros(T, Hkv * D, dtype=BF), v=torch.zeros(T, Hkv * D, dtype=BF),
+                   cu_seqlens=torch.tensor([0, T], dtype=I32), D=D, out=torch.zeros(T, Hq * D, dtype=BF), lse=torch.zeros(Hq, T)), **change}
+
+
+def test_rows_of_another_length_are_refused(lib):
+    """lse is read and written as [heads][T], u_accept as [N][L]: a wider matrix holds its rows elsewhere."""
+    with pytest.raises(ValueError):
+        hybrid.lfm2sc_attn_prefill(**_prompt(lse=torch.zeros(4, 16)))
+    a = _prompt(lse=torch.zeros(4, 16))
+    a.update(d_out=a["out"], dq=a["q"], dk=a["k"], dv=a["v"], workspace=torch.zeros(1 << 16, dtype=torch.uint8))
+    with pytest.raises(ValueError):
+        hybrid.lfm2sc_attn_backward(**a)
+    with pytest.raises(ValueError):
+        hybrid.lfm2sc_accept_drafts(**{**_drafts(), "u_accept": torch.zeros(3, 3)})
+    assert lib.calls == []
+
+
+def test_more_rows_and_flat_buffers_pass(lib):
+    hybrid.lfm2sc_attn_prefill(**_prompt(lse=torch.zeros(7, 10)))
+    hybrid.lfm2sc_attn_prefill(**_prompt(lse=torch.zeros(64)))
+    hybrid.lfm2sc_accept_drafts(**{**_drafts(), "u_accept": torch.zeros(8)})
+    hybrid.lfm2sc_accept_drafts(**{**_drafts(), "u_accept": torch.zeros(4, 2)})
+    assert len(lib.calls) == 4
