@@ -84,6 +84,12 @@ int check_ranges(const char* fn, hipStream_t s, const RangeCheck* checks, const 
     return LFM2SC_OK;
 }
 
+int submitted(const char* fn, hipError_t e) {
+    if (e == hipErrorInvalidConfiguration)
+        return fail(LFM2SC_ERR_BAD_SHAPE, "%s: the sizes need 2^32 or more work-items in one launch", fn);
+    return launched(fn, e);
+}
+
 size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
 
 size_t cached_bytes(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_keys) {
@@ -137,7 +143,7 @@ int lfm2sc_attn_prefill(int dtype, int D, int num_heads, int num_kv_heads, const
     a.total_T = total_T; a.cu = cu_seqlens; a.N = num_seqs;
     a.Hq = num_heads; a.Hkv = num_kv_heads; a.scale = scale;
     a.out = static_cast<uint16_t*>(out); a.out_stride = out_stride; a.lse = lse;
-    return launched(fn, launch_attn_prefill(a, D, s));
+    return submitted(fn, launch_attn_prefill(a, D, s));
 }
 
 size_t lfm2sc_attn_backward_workspace_bytes(int dtype, int D, int num_heads, int num_kv_heads, int64_t total_T,
@@ -201,7 +207,7 @@ int lfm2sc_attn_backward(int dtype, int D, int num_heads, int num_kv_heads, cons
     a.lse2 = reinterpret_cast<float*>(static_cast<char*>(workspace) + rows);
     a.splits = attn_backward_splits(num_heads, num_kv_heads, total_T, num_seqs);
     a.part = reinterpret_cast<float*>(static_cast<char*>(workspace) + 2 * rows);
-    return launched(fn, launch_attn_backward(a, D, s));
+    return submitted(fn, launch_attn_backward(a, D, s));
 }
 
 size_t lfm2sc_attn_cached_workspace_bytes(int dtype, int D, int num_heads, int num_kv_heads, int num_seqs, int L,
@@ -262,7 +268,7 @@ int lfm2sc_attn_cached(int dtype, int D, int num_heads, int num_kv_heads, const 
     a.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(rows * (size_t)D * 4));
     a.prefix_splits = a.prefix_chunk = a.suffix_splits = 0;
     a.prefix_blocks = 0;
-    return launched(fn, launch_attn_cached(a, D, s));
+    return submitted(fn, launch_attn_cached(a, D, s));
 }
 
 size_t lfm2sc_accept_drafts_workspace_bytes(int num_seqs, int L, int V) {
@@ -315,7 +321,7 @@ int lfm2sc_accept_drafts(int dtype, int V, int num_seqs, int L, const void* targ
         a.u_accept = u_accept; a.u_sample = u_sample;
         a.accept_len = accept_len; a.keep_len = keep_len; a.next_token = next_token;
         a.sums = static_cast<double*>(workspace);
-        return launched(fn, launch_drafts(a, s));
+        return submitted(fn, launch_drafts(a, s));
     };
     if (dtype == LFM2SC_BF16) {
         DraftArgs<uint16_t> a;

@@ -356,11 +356,10 @@ static hipError_t launch_bwd(const AttnGradArgs& a, hipStream_t s) {
     const AttnArgs& f = a.f;
     const int64_t rows = 32 * kGW, per_row = f.N == 1 ? (f.total_T + rows - 1) / rows : f.total_T / rows + f.N;
     const int64_t kv = per_row * f.Hkv * a.splits, all = kv * (kApart ? 2 : 1) + per_row * f.Hq;
-    const int64_t sums = f.total_T / 8 + f.N;
-    if (all >= ((int64_t)1 << 31) || sums >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+    const int64_t deltas = (f.total_T + 31) / 32, sums = a.splits > 1 ? f.total_T / 8 + f.N : 0;
+    if (too_many(all, 64 * kGW) || too_many(deltas, 256) || too_many(sums, 256)) return hipErrorInvalidConfiguration;
     const int heads = 64 / (D / 8);
-    hipLaunchKernelGGL((attn_delta_kernel<D>), dim3((uint32_t)((f.total_T + 31) / 32), (f.Hq + heads - 1) / heads), dim3(256),
-                       0, s, a);
+    hipLaunchKernelGGL((attn_delta_kernel<D>), dim3((uint32_t)deltas, (f.Hq + heads - 1) / heads), dim3(256), 0, s, a);
     hipLaunchKernelGGL((attn_grad_kernel<D, kGW, R, S, kApart>), dim3((uint32_t)all), dim3(64 * kGW), 0, s, a, (int)kv);
     if (a.splits > 1) hipLaunchKernelGGL((attn_dkv_sum_kernel<D>), dim3((uint32_t)sums), dim3(256), 0, s, a);
     return hipGetLastError();

@@ -461,14 +461,14 @@ CachedPlan cached_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int
 template <int D>
 static hipError_t launch_cached(const CachedArgs& a, const CachedPlan& p, hipStream_t s) {
     const int64_t blocks = p.prefix_blocks + p.suffix_blocks;
-    const int64_t joins = ((int64_t)a.N * a.L * a.Hq + 3) / 4;
-    if (blocks >= ((int64_t)1 << 31) || joins >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+    const int64_t joins = p.prefix_splits + p.suffix_splits > 1 ? ((int64_t)a.N * a.L * a.Hq + 3) / 4 : 0;
+    if (too_many(blocks, 64 * (p.direct ? kDirectW : kCW)) || too_many(joins, 256)) return hipErrorInvalidConfiguration;
     if (p.direct) {
         hipLaunchKernelGGL((attn_cached_direct_kernel<D>), dim3((uint32_t)blocks), dim3(64 * kDirectW), 0, s, a);
         return hipGetLastError();
     }
     hipLaunchKernelGGL((attn_cached_kernel<D>), dim3((uint32_t)blocks), dim3(64 * kCW), 0, s, a);
-    if (p.prefix_splits + p.suffix_splits > 1)
+    if (joins > 0)
         hipLaunchKernelGGL((attn_join_kernel<D>), dim3((uint32_t)joins), dim3(256), 0, s, a);
     return hipGetLastError();
 }

@@ -190,7 +190,7 @@ static hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
     // sum ceil(len / rows) over the sequences is at most this
     const int64_t rows = 32 * QB * W, per_head = a.N == 1 ? (a.total_T + rows - 1) / rows : a.total_T / rows + a.N;
     const int64_t blocks = per_head * a.Hq;
-    if (blocks >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+    if (too_many(blocks, 64 * W)) return hipErrorInvalidConfiguration;
     constexpr int kResident = 256 * (D == 64 ? 4 : 3);           // workgroups
     const int fold = a.N == 1 && blocks <= kResident ? 256 / a.Hq : 0;
     hipLaunchKernelGGL((attn_fwd_kernel<D, QB, W, KT, S>), dim3((uint32_t)blocks), dim3(64 * W), 0, s, a, fold);

@@ -407,6 +407,7 @@ hipError_t launch_drafts(const DraftArgs<E>& a, hipStream_t s) {
     constexpr int N = kWholeN<E>;
     const bool split = a.V > kWW * kWholeGroups * N * 512 || (a.N <= 32 && a.V > 65536);
     if (!split) {
+        if (too_many(a.N, 64 * kWW)) return hipErrorInvalidConfiguration;
         const dim3 grid(a.N), block(64 * kWW);
         if (a.V <= kWW * 512) hipLaunchKernelGGL((draft_whole_kernel<E, 1>), grid, block, 0, s, a);
         else if (a.V <= kWW * 4 * 512) hipLaunchKernelGGL((draft_whole_kernel<E, 4>), grid, block, 0, s, a);
@@ -414,7 +415,7 @@ hipError_t launch_drafts(const DraftArgs<E>& a, hipStream_t s) {
         return hipGetLastError();
     }
     const int chunks = draft_chunks(a.V);
-    if ((int64_t)chunks * a.N >= ((int64_t)1 << 31)) return hipErrorInvalidConfiguration;
+    if (too_many((int64_t)chunks * a.N, kDT)) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((draft_sums_kernel<E>), dim3((uint32_t)(chunks * a.N)), dim3(kDT), 0, s, a, chunks);
     hipLaunchKernelGGL((draft_pick_kernel<E>), dim3(a.N), dim3(64), 0, s, a, chunks);
     return hipGetLastError();

@@ -80,6 +80,10 @@ struct RangeCheck {
 };
 int check_device_ranges(hipStream_t s, const RangeCheck* checks, int count, hipError_t* err);
 
+// A launch holds fewer than 2^32 work-items a dimension.  The launchers below return
+// hipErrorInvalidConfiguration, before they launch anything, where a call needs more.
+inline bool too_many(int64_t blocks, int threads) { return blocks * threads >= (int64_t)1 << 32; }
+
 hipError_t launch_attn_prefill(const AttnArgs& a, int D, hipStream_t s);
 int attn_backward_splits(int Hq, int Hkv, int64_t total_T, int N);
 hipError_t launch_attn_backward(const AttnGradArgs& a, int D, hipStream_t s);

@@ -15,7 +15,9 @@
  * strides in elements, the same status codes, lfm2sc_last_error and
  * lfm2sc_status_string, LFM2SC_CHECK=1 for checks of device-side data.  Calls
  * launch kernels only (no memset, no copy), so they can be captured into a graph.
- * Results are deterministic: no atomics, every sum in a fixed order.
+ * Results are deterministic: no atomics, every sum in a fixed order.  Sizes that
+ * need 2^32 or more work-items in one launch (about 2^24 blocks of 32 to 128 rows
+ * times heads) are refused with LFM2SC_ERR_BAD_SHAPE.
  *
  * Attention, shared by its entry points
  * -------------------------------------
