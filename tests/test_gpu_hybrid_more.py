@@ -44,3 +44,71 @@ def test_drafts_entries_that_are_no_probabilities(V, dtype):
     target, draft = target.to(dtype), draft.to(dtype)
     for u in (0.0, 0.3, 0.77, 1 - 2 ** -24):
         _draft_calls(target, draft, tokens, torch.ones(N, 1), torch.full((N,), u))
+
+
+HALF = torch.finfo(BF).eps / 2
+U = 2.0 ** -24                                       # half an fp32 step, relative
+
+
+def _prompt64(q, k, v, cu, D, scale):
+    """out and lse in 64 bits on the GPU, with the magnitudes that their errors scale with.
+
+    An fp32 score is off by D sums of at most 2 U (rounded or cut) of scale sum |q||k|, by 3 U of its value from scale, log2 e
+    and their product, by U of its value from the subtraction of the reference and by 2 U from exp2: terms(scale sum |q||k|)
+    below.  lse takes these errors weighted with p; its sum of the exponentials adds one rounding per term of a tile of at
+    most 64 keys and of a half's 32, and up to 4 per tile (sum, rescaling and its factor); the logarithm, the reference
+    (within 16 of lse in base 2) and their sum add 8 U |lse| + 32 U.  out takes each p's error from its row's largest score
+    terms, and the sum's error once more.
+    """
+    T, Hq, Hkv = q.shape[0], q.shape[1] // D, k.shape[1] // D
+    q, k, v = q.double(), k.double(), v.double()
+    out, spread = (torch.full((T, Hq * D), float("nan"), dtype=torch.float64, device=DEV) for _ in range(2))
+    lse, lse_tol, p_tol = (torch.full((Hq, T), float("nan"), dtype=torch.float64, device=DEV) for _ in range(3))
+    cu = cu.tolist()
+    for a, b in zip(cu, cu[1:]):
+        if a == b:
+            continue
+        future = torch.ones(b - a, b - a, dtype=torch.bool, device=DEV).triu(1)
+        sums = 40 + 4 * (torch.arange(b - a, device=DEV) // 32 + 1)
+        for h in range(Hq):
+            c, kc = slice(h * D, h * D + D), slice(h // (Hq // Hkv) * D, h // (Hq // Hkv) * D + D)
+            s = (scale * (q[a:b, c] @ k[a:b, kc].t())).masked_fill(future, float("-inf"))
+            terms = (scale * (q[a:b, c].abs() @ k[a:b, kc].abs().t())).masked_fill(future, 0)
+            p, z = torch.softmax(s, 1), torch.logsumexp(s, 1)
+            out[a:b, c], spread[a:b, c], lse[h, a:b] = p @ v[a:b, kc], p @ v[a:b, kc].abs(), z
+            lse_tol[h, a:b] = U * ((2 * D + 8) * (p * terms).sum(1) + 8 * z.abs() + 40 + sums)
+            p_tol[h, a:b] = U * (2 * (2 * D + 8) * terms.amax(1) + 40 + sums)
+    return out, spread, lse, lse_tol, p_tol.t().repeat_interleave(D, 1)
+
+
+def _check_prompt(lens, Hq, Hkv, D, scale, amp=1.0, seed=0):
+    gen = torch.Generator().manual_seed(seed)
+    T = sum(lens)
+    q = (torch.randn(T, Hq * D, generator=gen) * amp).to(BF).to(DEV)
+    kv = torch.randn(T, 2 * Hkv * D, generator=gen).to(BF).to(DEV)
+    k, v = kv[:, :Hkv * D], kv[:, Hkv * D:]
+    cu = torch.tensor([0] + lens).cumsum(0).to(I32)
+    out, lse = torch.full_like(q, float("nan")), torch.full((Hq, T), float("nan"), device=DEV)
+    g.lfm2sc_attn_prefill(q, k, v, cu.to(DEV), D, out, lse=lse, scale=scale)
+    want, spread, wlse, lse_tol, p_tol = _prompt64(q, k, v, cu, D, scale)
+    off = (lse.double() - wlse).abs() / lse_tol
+    assert (off <= 1).all(), ("lse", float(off.nan_to_num(9e9).max()))
+    off = (out.double() - want).abs() / (HALF * (spread + want.abs()) + p_tol * spread)
+    assert (off <= 1).all(), ("out", float(off.nan_to_num(9e9).max()))
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [([1], 8, 2, 128), ([2, 1, 3], 4, 1, 64), ([63], 2, 2, 64), ([65], 2, 1, 128), ([127, 1, 0, 128], 4, 2, 64),
+                                           ([129, 31, 97], 6, 2, 128), ([300, 2], 12, 1, 64), ([33] * 90, 16, 8, 128), ([700], 9, 3, 128),
+                                           ([1111], 2, 1, 64)])
+@pytest.mark.parametrize("amp", [1.0, 30.0])
+def test_prompt_lse_to_fp32(lens, Hq, Hkv, D, amp):
+    """lse and out within what fp32 scores and sums leave; amp 30: scores of hundreds, most probabilities vanish."""
+    _check_prompt(lens, Hq, Hkv, D, D ** -0.5, amp, seed=len(lens))
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D", [(2100, 32, 8, 64), (4001, 32, 8, 64), (3333, 24, 8, 64), (5400, 12, 1, 64), (2051, 32, 4, 128),
+                                        (3001, 32, 8, 128), (4500, 16, 2, 128)])
+def test_prompt_one_sequence_of_many_row_blocks(T, Hq, Hkv, D):
+    """One sequence whose workgroups are all resident: every other round of 256 / heads row blocks of 128 runs the other
+    way, unless it is incomplete (2100, 3333, 5400, 2051 and 4500 tokens end in such a round)."""
+    _check_prompt([T], Hq, Hkv, D, D ** -0.5, seed=T)
