@@ -89,7 +89,6 @@ __device__ __forceinline__ void kv_part(const AttnGradArgs& a, X qslot, Y dslot,
     constexpr int kPer = 2 * decltype(qcopy)::kDma + (kK ? 2 : 1);       // copies of a tile per wave
     issue(qslot(IC<0>{}), dslot(IC<0>{}), zslot(IC<0>{}), 0);
     if constexpr (S > 2) issue(qslot(IC<1>{}), dslot(IC<1>{}), zslot(IC<1>{}), 1);
-    if constexpr (S > 3) issue(qslot(IC<2>{}), dslot(IC<2>{}), zslot(IC<2>{}), 2);
 
     bf16x8 kf[D / 16], vf[D / 16];
     const bool exists = wkey + c < st.len;
@@ -241,7 +240,6 @@ __device__ __forceinline__ void dq_part(const AttnGradArgs& a, X kslot, Y vslot,
     };
     issue(kslot(IC<0>{}), vslot(IC<0>{}), 0);
     if constexpr (S > 2) issue(kslot(IC<1>{}), vslot(IC<1>{}), 1);
-    if constexpr (S > 3) issue(kslot(IC<2>{}), vslot(IC<2>{}), 2);
 
     bf16x8 qf[D / 16], df[D / 16];
     const bool exists = wrow + c < st.len;
@@ -316,11 +314,10 @@ __global__ __launch_bounds__(64 * W, 2) void attn_grad_kernel(AttnGradArgs a, in
     // a variable per slot: the compiler then knows which reads a copy in flight cannot touch
     __shared__ __attribute__((aligned(1024))) uint8_t x0[kTileB], x1[kTileB], y0[kTileB], y1[kTileB];
     __shared__ __attribute__((aligned(1024))) uint8_t x2[S > 2 ? kTileB : 16], y2[S > 2 ? kTileB : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t x3[S > 3 ? kTileB : 16], y3[S > 3 ? kTileB : 16];
-    __shared__ __attribute__((aligned(1024))) float z0[kZ], z1[kZ], z2[S > 2 ? kZ : 4], z3[S > 3 ? kZ : 4];
-    auto x = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(x0, x1, x2, x3); };
-    auto y = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(y0, y1, y2, y3); };
-    auto z = [&](auto u) -> float* { return pick_slot<decltype(u)::value>(z0, z1, z2, z3); };
+    __shared__ __attribute__((aligned(1024))) float z0[kZ], z1[kZ], z2[S > 2 ? kZ : 4];
+    auto x = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(x0, x1, x2); };
+    auto y = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(y0, y1, y2); };
+    auto z = [&](auto u) -> float* { return pick_slot<decltype(u)::value>(z0, z1, z2); };
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     const int b = blockIdx.x;

@@ -20,7 +20,6 @@ constexpr int kCRows = 32 * kCW;              // query rows of a prefix workgrou
 constexpr int kPrefixTile = 64;               // keys per staged tile, prefix
 constexpr int kOwnTile = 32;                  // keys per wave's tile, suffix
 constexpr int kDirectW = 8;                   // waves per workgroup of the direct form
-constexpr float kLazy = 8.f;                  // as in attn_fwd.hip: how far (log2) a maximum may pass the reference
 
 // Row number in the pool of key idx (< 2^31), whose page number is `page`.  A
 // page number outside the pool reads as the nearest page of it.  The number is

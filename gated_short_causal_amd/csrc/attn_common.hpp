@@ -26,6 +26,11 @@ constexpr float kLog2e = 1.44269504088896340736f;
 constexpr float kLn2 = 0.69314718055994530942f;
 constexpr float kNegInf = -__builtin_inff();
 
+// How far (log2) a row's maximum may pass the reference m of its softmax before
+// the reference moves: most tiles then rescale nothing, and p stays below
+// 2^kLazy, whose bf16 and fp32 values are as exact as those below 1.
+constexpr float kLazy = 8.f;
+
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // The value of the lane 32 away, for a reduction over both halves of a wave.
@@ -141,27 +146,24 @@ struct TileCopy {
     }
 };
 
-// A ring of S staged tiles: step(IC<u>, t) for t = 0 .. n - 1 with u = t % S.  The
+// A ring of S (2 or 3) staged tiles: step(IC<u>, t) for t = 0 .. n - 1 with u = t % S.  The
 // step waits for tile t, meets the workgroup, refills slot (u + S - 1) % S with
 // tile min(t + S - 1, n - 1) (always, so that the number of copies in flight at
 // every wait is a constant) and computes from slot u.
 template <int u, typename T>
-__device__ __forceinline__ T* pick_slot(T* a, T* b, T* c, T* d) {
+__device__ __forceinline__ T* pick_slot(T* a, T* b, T* c) {
     if constexpr (u == 0) return a;
     else if constexpr (u == 1) return b;
-    else if constexpr (u == 2) return c;
-    else return d;
+    else return c;
 }
 template <int S, typename F>
 __device__ __forceinline__ void for_stages(int n, F step) {
+    static_assert(S == 2 || S == 3, "slots");
     for (int t = 0; t < n; t += S) {
         step(IC<0>{}, t);
         if (t + 1 < n) step(IC<1>{}, t + 1);
         if constexpr (S > 2) {
             if (t + 2 < n) step(IC<2>{}, t + 2);
-        }
-        if constexpr (S > 3) {
-            if (t + 3 < n) step(IC<3>{}, t + 3);
         }
     }
 }

@@ -1,7 +1,7 @@
 // attn_fwd.hip -- causal attention over packed prompts, grouped heads.
 //
 // One pass over the keys with the running maximum m and sum l of each query
-// row's softmax.  A wave owns 32 QB query rows of one head; a workgroup's W
+// row's softmax.  A wave owns 32 query rows of one head; a workgroup's W
 // waves own consecutive rows and share the K and V tiles (kKT keys) that are
 // copied to LDS ahead of use, S slots of them.  Scores are formed transposed, S^T = K Q^T, so
 // that a lane holds 16 keys of one query per 32-key block: the row maximum and
@@ -24,8 +24,6 @@
 
 namespace lfm2sc {
 
-constexpr float kLazy = 8.f;      // how far (log2) a row's maximum may pass its reference m
-
 // A launch of one sequence whose workgroups are all resident at once: CU i gets
 // blocks i, i + 256, .. in falling order, so the CUs with the first of each
 // round would get all the heavy ones.  Every other round of `fold` row blocks
@@ -36,17 +34,16 @@ __device__ __forceinline__ int folded(int t, int blocks, int fold) {
     return (round & 1) && (round + 1) * fold <= blocks ? round * fold + fold - 1 - t % fold : t;
 }
 
-template <int D, int QB, int W, int kKT, int S>
+template <int D, int W, int kKT, int S>
 __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a, int fold) {
     using T = Tile<D>;
-    constexpr int kBM = 32 * QB * W, NB = kKT / 32;
+    constexpr int kBM = 32 * W, NB = kKT / 32;
     constexpr int kTileB = kKT * T::kRowB;
     // a variable per slot: the compiler then knows which reads a copy in flight cannot touch
     __shared__ __attribute__((aligned(1024))) uint8_t k0[kTileB], k1[kTileB], v0[kTileB], v1[kTileB];
     __shared__ __attribute__((aligned(1024))) uint8_t k2[S > 2 ? kTileB : 16], v2[S > 2 ? kTileB : 16];
-    __shared__ __attribute__((aligned(1024))) uint8_t k3[S > 3 ? kTileB : 16], v3[S > 3 ? kTileB : 16];
-    auto kslot = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(k0, k1, k2, k3); };
-    auto vslot = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(v0, v1, v2, v3); };
+    auto kslot = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(k0, k1, k2); };
+    auto vslot = [&](auto u) -> uint8_t* { return pick_slot<decltype(u)::value>(v0, v1, v2); };
 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63, c = lane & 31, h = lane >> 5;
@@ -58,7 +55,7 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a, int fol
     const SeqTile st = find_seq_tile(a.cu, a.N, a.total_T, folded(b / a.Hq, gridDim.x / a.Hq, fold), kBM);
     if (st.len == 0) return;
     const int q0 = (st.rank - 1) * kBM;
-    const int wrow = q0 + wave * 32 * QB;        // the wave's first row in the sequence
+    const int wrow = q0 + wave * 32;             // the wave's first row in the sequence
     const int tiles = (min(q0 + kBM, st.len) + kKT - 1) / kKT;
 
     const uint16_t* kp = a.k + st.start * a.k_stride + (int64_t)kvh * D;
@@ -73,99 +70,71 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a, int fol
 
     issue(k0, v0, 0);
     if constexpr (S > 2) issue(k1, v1, 1);
-    if constexpr (S > 3) issue(k2, v2, 2);
 
-    // the wave's queries as B operands: row c of each block, values 16 s + 8 h ..
-    bf16x8 qf[QB][D / 16];
-#pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
-        const int r = wrow + qb * 32 + c;
-        load_row_operand<D>(qf[qb], a.q + (st.start + r) * a.q_stride + (int64_t)head * D, h, r < st.len);
-    }
+    // the wave's queries as B operands: row c, values 16 s + 8 h ..
+    bf16x8 qf[D / 16];
+    const int row = wrow + c;
+    load_row_operand<D>(qf, a.q + (st.start + row) * a.q_stride + (int64_t)head * D, h, row < st.len);
     const LaneOffsets<D> lo(lane);
     const float cs = a.scale * kLog2e;           // exp(scale s) = exp2(cs s)
-    float m[QB], l[QB];
-    f32x16 o[QB][D / 32];
+    float m = kNegInf, l = 0.f;
+    f32x16 o[D / 32];
 #pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
-        m[qb] = kNegInf;
-        l[qb] = 0.f;
+    for (int db = 0; db < D / 32; ++db)
 #pragma unroll
-        for (int db = 0; db < D / 32; ++db)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[qb][db][i] = 0.f;
-    }
+        for (int i = 0; i < 16; ++i) o[db][i] = 0.f;
 
     auto tile = [&](const uint8_t* kb, const uint8_t* vb, int t) {
-        f32x16 s[QB][NB];
-#pragma unroll
-        for (int qb = 0; qb < QB; ++qb)
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[qb][n][i] = 0.f;
+        f32x16 s[NB];
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
-            for (int ds = 0; ds < D / 16; ++ds) {
-                const bf16x8 kf = lds_row(kb + n * 32 * T::kRowB, lo.row[ds]);
+            for (int i = 0; i < 16; ++i) s[n][i] = 0.f;
 #pragma unroll
-                for (int qb = 0; qb < QB; ++qb) s[qb][n] = mfma32(kf, qf[qb][ds], s[qb][n]);
-            }
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int ds = 0; ds < D / 16; ++ds) s[n] = mfma32(lds_row(kb + n * 32 * T::kRowB, lo.row[ds]), qf[ds], s[n]);
         if (t * kKT + kKT - 1 > wrow) {          // the tile reaches past the wave's first row
+            const int r = row - t * kKT - 4 * h;
 #pragma unroll
-            for (int qb = 0; qb < QB; ++qb) {
-                const int r = wrow + qb * 32 + c - t * kKT - 4 * h;
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int n = 0; n < NB; ++n)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (n * 32 + (i & 3) + 8 * (i >> 2) > r) s[qb][n][i] = kNegInf;
-            }
+                for (int i = 0; i < 16; ++i)
+                    if (n * 32 + (i & 3) + 8 * (i >> 2) > r) s[n][i] = kNegInf;
         }
+        float mx = s[0][0];
 #pragma unroll
-        for (int qb = 0; qb < QB; ++qb) {
-            float mx = s[qb][0][0];
+        for (int i = 1; i < 16 * NB; ++i) mx = fmaxf(mx, s[i >> 4][i & 15]);
+        const float mn = max_halves(mx) * cs;
+        if (__any(mn > m + kLazy)) {
+            const float ref = fmaxf(m, mn), alpha = exp2_fast(m - ref);
+            l *= alpha;
 #pragma unroll
-            for (int i = 1; i < 16 * NB; ++i) mx = fmaxf(mx, s[qb][i >> 4][i & 15]);
-            // m is a reference, not the maximum: it moves only when a row's maximum passes it by 2^kLazy, so most tiles
-            // rescale nothing.  p stays below 2^kLazy, whose bf16 and fp32 values are as exact as those below 1.
-            const float mn = max_halves(mx) * cs;
-            if (__any(mn > m[qb] + kLazy)) {
-                const float ref = fmaxf(m[qb], mn), alpha = exp2_fast(m[qb] - ref);
-                l[qb] *= alpha;
+            for (int db = 0; db < D / 32; ++db)
 #pragma unroll
-                for (int db = 0; db < D / 32; ++db)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[qb][db][i] *= alpha;
-                m[qb] = ref;
-            }
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16 * NB; ++i) {
-                const float p = exp2_fast(__builtin_fmaf(s[qb][i >> 4][i & 15], cs, -m[qb]));
-                s[qb][i >> 4][i & 15] = p;
-                sum += p;
-            }
-            l[qb] += sum;
+                for (int i = 0; i < 16; ++i) o[db][i] *= alpha;
+            m = ref;
         }
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16 * NB; ++i) {
+            const float p = exp2_fast(__builtin_fmaf(s[i >> 4][i & 15], cs, -m));
+            s[i >> 4][i & 15] = p;
+            sum += p;
+        }
+        l += sum;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 p[QB];
+                const bf16x8 p = to_operand(s[n], ks);
 #pragma unroll
-                for (int qb = 0; qb < QB; ++qb) p[qb] = to_operand(s[qb][n], ks);
-#pragma unroll
-                for (int db = 0; db < D / 32; ++db) {
-                    const bf16x8 vf = lds_transposed(vb + (n * 32 + ks * 16) * T::kRowB, lo.tr[0][db], lo.tr[1][db]);
-#pragma unroll
-                    for (int qb = 0; qb < QB; ++qb) o[qb][db] = mfma32(vf, p[qb], o[qb][db]);
-                }
+                for (int db = 0; db < D / 32; ++db)
+                    o[db] = mfma32(lds_transposed(vb + (n * 32 + ks * 16) * T::kRowB, lo.tr[0][db], lo.tr[1][db]), p, o[db]);
             }
     };
 
-    const int last = min(wrow + 32 * QB, st.len) - 1;    // the wave's last row
+    const int last = min(wrow + 32, st.len) - 1;    // the wave's last row
     for_stages<S>(tiles, [&](auto u, int t) {
         constexpr int refill = (decltype(u)::value + S - 1) % S;
         wait_vm<(S - 2) * 2 * decltype(kcopy)::kDma>();
@@ -175,32 +144,28 @@ __global__ __launch_bounds__(64 * W, 2) void attn_fwd_kernel(AttnArgs a, int fol
     });
     wait_vm<0>();                                // no copy may outlive the workgroup
 
-#pragma unroll
-    for (int qb = 0; qb < QB; ++qb) {
-        const int r = wrow + qb * 32 + c;
-        const float sum = sum_halves(l[qb]);
-        store_transposed<D>(a.out + (st.start + r) * a.out_stride + (int64_t)head * D, o[qb], 1.f / sum, h, r < st.len);
-        if (a.lse != nullptr && h == 0 && r < st.len)
-            a.lse[(int64_t)head * a.total_T + st.start + r] = (m[qb] + __builtin_amdgcn_logf(sum)) * kLn2;
-    }
+    const float sum = sum_halves(l);
+    store_transposed<D>(a.out + (st.start + row) * a.out_stride + (int64_t)head * D, o, 1.f / sum, h, row < st.len);
+    if (a.lse != nullptr && h == 0 && row < st.len)
+        a.lse[(int64_t)head * a.total_T + st.start + row] = (m + __builtin_amdgcn_logf(sum)) * kLn2;
 }
 
-template <int D, int QB, int W, int KT, int S>
+template <int D, int W, int KT, int S>
 static hipError_t launch_fwd(const AttnArgs& a, hipStream_t s) {
     // sum ceil(len / rows) over the sequences is at most this
-    const int64_t rows = 32 * QB * W, per_head = a.N == 1 ? (a.total_T + rows - 1) / rows : a.total_T / rows + a.N;
+    const int64_t rows = 32 * W, per_head = a.N == 1 ? (a.total_T + rows - 1) / rows : a.total_T / rows + a.N;
     const int64_t blocks = per_head * a.Hq;
     if (too_many(blocks, 64 * W)) return hipErrorInvalidConfiguration;
     constexpr int kResident = 256 * (D == 64 ? 4 : 3);           // workgroups
     const int fold = a.N == 1 && blocks <= kResident ? 256 / a.Hq : 0;
-    hipLaunchKernelGGL((attn_fwd_kernel<D, QB, W, KT, S>), dim3((uint32_t)blocks), dim3(64 * W), 0, s, a, fold);
+    hipLaunchKernelGGL((attn_fwd_kernel<D, W, KT, S>), dim3((uint32_t)blocks), dim3(64 * W), 0, s, a, fold);
     return hipGetLastError();
 }
 
 hipError_t launch_attn_prefill(const AttnArgs& a, int D, hipStream_t s) {
     // keys per tile and slots: D = 64 leaves four workgroups per CU with two slots of 64 keys (8 x 2048: 56.3 us; 32, 3
     // and 64, 3 60), D = 128 three with three slots of 32 (13 x 1531: 52.1 us; 32, 2 54.0; 32, 4 57.6; 64, 2 56.2)
-    return D == 64 ? launch_fwd<64, 1, 4, 64, 2>(a, s) : launch_fwd<128, 1, 4, 32, 3>(a, s);
+    return D == 64 ? launch_fwd<64, 4, 64, 2>(a, s) : launch_fwd<128, 4, 32, 3>(a, s);
 }
 
 }  // namespace lfm2sc
