@@ -13,6 +13,7 @@ using namespace lfm2sc;
 
 constexpr int64_t kMaxRowStride = (int64_t)1 << 22;   // 64 rows of a tile stay within 32-bit byte offsets
 constexpr int kMaxHeads = 1 << 14;
+constexpr int64_t kMaxCachedRows = (int64_t)1 << 28;
 constexpr int64_t kMaxKeys = (int64_t)1 << 30;        // a tile past a sequence's end still counts in an int
 
 int check_heads(const char* fn, int dtype, int D, int Hq, int Hkv) {
@@ -98,9 +99,16 @@ size_t cached_bytes(int D, int Hq, int Hkv, int N, int L, int prefix_len, int ma
     return round_up(rows * (size_t)D * 4) + round_up(rows * 8);
 }
 
+// rows and heads of the new tokens within the kernels' int counters (each factor is at most 2^31, so no product here
+// passes 64 bits)
+bool cached_rows_fit(int N, int L, int Hq) {
+    const int64_t rows = (int64_t)N * L;
+    return rows < kMaxCachedRows && rows * Hq < kMaxCachedRows;
+}
+
 int check_cached_sizes(const char* fn, int N, int L, int Hq, int prefix_len, int max_pages, int page_size) {
     if (N < 0 || L < 0) return fail(LFM2SC_ERR_BAD_SHAPE, "%s: num_seqs=%d or L=%d is negative", fn, N, L);
-    if ((int64_t)N * L * Hq >= ((int64_t)1 << 28))
+    if (!cached_rows_fit(N, L, Hq))
         return fail(LFM2SC_ERR_BAD_SHAPE, "%s: num_seqs * L * num_heads is 2^28 or more", fn);
     if (prefix_len < 0 || prefix_len >= kMaxKeys)
         return fail(LFM2SC_ERR_BAD_SHAPE, "%s: prefix_len=%d outside [0, 2^30)", fn, prefix_len);
@@ -214,7 +222,7 @@ size_t lfm2sc_attn_cached_workspace_bytes(int dtype, int D, int num_heads, int n
                                           int prefix_len, int max_pages, int page_size) {
     if (dtype != LFM2SC_BF16 || (D != 64 && D != 128) || num_kv_heads < 1 || num_heads < num_kv_heads ||
         num_heads % num_kv_heads != 0 || num_heads > kMaxHeads || num_seqs <= 0 || L <= 0 ||
-        (int64_t)num_seqs * L * num_heads >= ((int64_t)1 << 28) || prefix_len < 0 || prefix_len >= kMaxKeys ||
+        !cached_rows_fit(num_seqs, L, num_heads) || prefix_len < 0 || prefix_len >= kMaxKeys ||
         page_size < 1 || (page_size & (page_size - 1)) != 0 || max_pages < 0 || (int64_t)max_pages * page_size >= kMaxKeys)
         return 0;
     return cached_bytes(D, num_heads, num_kv_heads, num_seqs, L, prefix_len, max_pages * page_size);

@@ -38,3 +38,30 @@ def test_cached(L, N, block, H, Hkv, prefix):
 def test_drafts(L):
     N = 1 << 22                                     # a workgroup of 1024 each
     assert L.lfm2sc_accept_drafts(1, 16, N, 1, P, 16, P, 16, P, P, P, P, P, P, P, P, HUGE, None) == SHAPE
+
+
+def test_workspace_queries_at_extreme_sizes(L):
+    """Sizes are computed in 64 bits: never negative or wrapped (the caller would allocate too little)."""
+    ends = (-(1 << 31), -1, 0, 1, 31, 1 << 14, (1 << 24) - 1, (1 << 30) - 1, 1 << 30, (1 << 31) - 1)
+    for H, Hkv in ((1, 1), (32, 8), (1 << 14, 1), (1 << 14, 1 << 14)):
+        for n in ends:
+            for T in ends + (1 << 40,):
+                got = L.lfm2sc_attn_backward_workspace_bytes(0, 128, H, Hkv, T, n)
+                valid = n > 0 and 0 < T < 1 << 30
+                assert (got >= 8 * H * T) if valid else got == 0, (H, Hkv, T, n)
+            for block in ends:
+                for prefix in ends:
+                    for pages, page in ((0, 16), (1, 1 << 29), (1 << 25, 16), (1 << 29, 4), (-1, 16), (4, 12)):
+                        got = L.lfm2sc_attn_cached_workspace_bytes(0, 128, H, Hkv, n, block, prefix, pages, page)
+                        valid = (n > 0 and block > 0 and n * block * H < 1 << 28 and 0 <= prefix < 1 << 30 and pages >= 0
+                                 and page & (page - 1) == 0 and pages * page < 1 << 30)
+                        assert valid or got == 0, (H, n, block, prefix, pages, page)
+                        # the split form keeps at least one partial row of D and a pair per row of each part
+                        assert got == 0 or got >= n * block * H * (128 * 4 + 8), (H, n, block, prefix, pages, page)
+
+
+@pytest.mark.parametrize("N,block,H", [(1 << 20, 1 << 30, 1 << 14), ((1 << 31) - 1, (1 << 31) - 1, 32), (1 << 30, 1 << 30, 16)])
+def test_cached_sizes_whose_product_passes_64_bits(L, N, block, H):
+    assert L.lfm2sc_attn_cached_workspace_bytes(0, 64, H, 1, N, block, 500, 4, 16) == 0
+    assert L.lfm2sc_attn_cached(0, 64, H, 1, P, H * 64, N, block, P, P, 64, 1000, 16, P, 500, P, 4, P, 0.125, P, H * 64, P, HUGE,
+                                None) == SHAPE
