@@ -13,6 +13,7 @@ using namespace lfm2sc;
 
 constexpr int64_t kMaxRowStride = (int64_t)1 << 22;   // 64 rows of a tile stay within 32-bit byte offsets
 constexpr int kMaxHeads = 1 << 14;
+constexpr int kMaxV = 1 << 30;                        // a row's byte offsets are 32-bit
 constexpr int64_t kMaxCachedRows = (int64_t)1 << 28;
 constexpr int64_t kMaxKeys = (int64_t)1 << 30;        // a tile past a sequence's end still counts in an int
 
@@ -280,7 +281,7 @@ int lfm2sc_attn_cached(int dtype, int D, int num_heads, int num_kv_heads, const 
 }
 
 size_t lfm2sc_accept_drafts_workspace_bytes(int num_seqs, int L, int V) {
-    if (num_seqs <= 0 || L < 0 || L > 64 || V < 1) return 0;
+    if (num_seqs <= 0 || L < 0 || L > 64 || V < 1 || V >= kMaxV) return 0;
     return round_up((size_t)num_seqs * 2 * (size_t)draft_chunks(V) * 8);
 }
 
@@ -291,7 +292,7 @@ int lfm2sc_accept_drafts(int dtype, int V, int num_seqs, int L, const void* targ
     const char* fn = "lfm2sc_accept_drafts";
     if (dtype != LFM2SC_BF16 && dtype != LFM2SC_F32)
         return fail(LFM2SC_ERR_UNSUPPORTED, "%s: dtype %d is neither LFM2SC_BF16 (0) nor LFM2SC_F32 (1)", fn, dtype);
-    if (V < 1 || V >= (1 << 30)) return fail(LFM2SC_ERR_BAD_SHAPE, "%s: V=%d outside [1, 2^30)", fn, V);
+    if (V < 1 || V >= kMaxV) return fail(LFM2SC_ERR_BAD_SHAPE, "%s: V=%d outside [1, 2^30)", fn, V);
     if (L < 0 || L > 64) return fail(LFM2SC_ERR_BAD_SHAPE, "%s: L=%d outside [0, 64]", fn, L);
     if (num_seqs < 0) return fail(LFM2SC_ERR_BAD_SHAPE, "%s: num_seqs=%d is negative", fn, num_seqs);
     if ((int64_t)num_seqs * draft_chunks(V) >= kMaxRows)

@@ -163,7 +163,7 @@ size_t lfm2sc_accept_drafts_workspace_bytes(int num_seqs, int L, int V);
  *              is never accepted).  For
  *              u_sample outside [0, 1) the last j with r_j > 0 (or, below 0, the
  *              first); -1 when the row has no positive entry.
- * 0 <= L <= 64, V >= 1; strides >= V, rows need only be aligned to an element.
+ * 0 <= L <= 64, 1 <= V < 2^30; strides >= V, rows need only be aligned to an element.
  * draft_probs, draft_tokens and u_accept may be NULL when L is 0.
  * workspace    8-byte aligned.
  */

@@ -65,3 +65,14 @@ def test_cached_sizes_whose_product_passes_64_bits(L, N, block, H):
     assert L.lfm2sc_attn_cached_workspace_bytes(0, 64, H, 1, N, block, 500, 4, 16) == 0
     assert L.lfm2sc_attn_cached(0, 64, H, 1, P, H * 64, N, block, P, P, 64, 1000, 16, P, 500, P, 4, P, 0.125, P, H * 64, P, HUGE,
                                 None) == SHAPE
+
+
+def test_draft_workspace_query_at_extreme_sizes(L):
+    ends = (-(1 << 31), -1, 0, 1, 4096, 4097, (1 << 30) - 1, 1 << 30, (1 << 31) - 4096, (1 << 31) - 1)
+    for n in ends:
+        for V in ends:
+            got = L.lfm2sc_accept_drafts_workspace_bytes(n, 4, V)
+            if n > 0 and 0 < V < 1 << 30:
+                assert n * 2 * -(-V // 4096) * 8 <= got < n * 2 * -(-V // 4096) * 8 + 256, (n, V)
+            else:
+                assert got == 0, (n, V)
