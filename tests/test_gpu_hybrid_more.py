@@ -5,6 +5,7 @@ import torch
 
 import gated_short_causal_amd as g
 from oracle import hybrid as ho
+from test_gpu_hybrid import _pages, _run_cached, _slack, _within
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -112,3 +113,35 @@ def test_prompt_one_sequence_of_many_row_blocks(T, Hq, Hkv, D):
     """One sequence whose workgroups are all resident: every other round of 256 / heads row blocks of 128 runs the other
     way, unless it is incomplete (2100, 3333, 5400, 2051 and 4500 tokens end in such a round)."""
     _check_prompt([T], Hq, Hkv, D, D ** -0.5, seed=T)
+
+
+def _check_cached(lens, L, prefix, S, Hq, Hkv, D, most=None, seed=0):
+    """Against the oracle; a page table of `most` pages a sequence, its unused entries no page numbers."""
+    kv, pp, table = _pages(np.random.default_rng(seed), len(lens), lens, prefix, S, Hkv, D)
+    if most is not None:
+        wide = torch.full((len(lens), most), -1, dtype=I32)
+        wide[:, 1::2] = 1 << 30
+        wide[:, :table.shape[1]] = table
+        for i, n in enumerate(lens):
+            wide[i, -(-n // S):table.shape[1]] = -7
+        table = wide
+    q = torch.randn(len(lens) * L, Hq * D, generator=torch.Generator().manual_seed(seed)).to(BF)
+    scale = D ** -0.5
+    out = _run_cached(q, kv, pp, prefix, table, lens, L, D, scale, False)
+    want, spread = ho.cached(q, kv[:, :, 0], kv[:, :, 1], pp, prefix, table.clamp(0, kv.shape[0] - 1), lens, L, scale)
+    slack = _slack(q, torch.nan_to_num(kv.float()), D, scale)
+    _within(out, want, HALF * (spread + np.abs(want)) + slack * spread, "out")
+
+
+@pytest.mark.parametrize("lens,L,prefix,S,Hq,Hkv,D", [([37], 1, 500, 16, 32, 8, 64), ([5, 64, 200, 0], 1, 63, 16, 8, 2, 64), ([300, 1], 1, 0, 16, 4, 2, 128),
+                                                      ([8, 9, 130], 8, 65, 64, 10, 2, 128), ([40] * 70, 1, 700, 32, 8, 2, 64)])
+def test_cached_tables_wider_than_the_sequences(lens, L, prefix, S, Hq, Hkv, D):
+    """A table of the longest context a server allows (32768 keys): most of its splits hold no key."""
+    _check_cached(lens, L, prefix, S, Hq, Hkv, D, most=32768 // S)
+
+
+@pytest.mark.parametrize("lens,L,prefix,S,Hq,Hkv,D", [([200, 150, 401], 150, 100, 16, 4, 2, 64), ([333], 333, 0, 32, 3, 1, 128), ([70, 600, 129], 129, 0, 16, 4, 4, 64),
+                                                      ([140, 20, 0], 140, 1000, 64, 2, 1, 128)])
+def test_cached_long_blocks(lens, L, prefix, S, Hq, Hkv, D):
+    """Blocks of more tokens than a row block has rows; sequences shorter than the block."""
+    _check_cached(lens, L, prefix, S, Hq, Hkv, D)
