@@ -10,10 +10,16 @@
 // the group's heads and queries stream past), one by query blocks (dq stays,
 // keys stream).  Both form p again from q, k and lse: 7 products for the 5 that the
 // formulas need (8 where dk and dv go apart).  Per executed product the long case is
-// near what a library product reaches (T = 8192, 32 / 8 heads of 64: 889 us = 1.08
-// PFLOP/s executed, 0.77 of the formulas' five); D = 128 waits more (two waves per
+// near what a library product reaches (T = 8192, 32 / 8 heads of 64: 889-927 us = 1.04-1.08
+// PFLOP/s executed, 0.74-0.77 of the formulas' five); D = 128 waits more (two waves per
 // SIMD, 37% of the cycles in the matrix unit).  dq summed with atomics would save
 // two products and the bits' order.
+//
+// Fewer bits: p and ds are operands of a second product and enter it rounded to
+// bf16 once (2^-9 of each), and delta takes the output as the caller holds it, in
+// bf16.  Gradients are off by 2.5e-3 (relative 2-norm) where their own rounding
+// alone gives 1.7e-3; ds in two bf16 parts would need two more products.  p, dp,
+// ds up to there, delta and all sums are fp32.
 #include "attn_common.hpp"
 #include "hybrid.hpp"
 

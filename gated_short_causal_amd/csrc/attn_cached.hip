@@ -9,7 +9,9 @@
 // unnormalised output in the workspace, and a second kernel joins them:
 //   out = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i,   m = max m_i.
 // One launch holds the workgroups of both kinds, the prefix's first (they run
-// longest).  All sums are fp32; p is rounded to bf16 for the product with v.
+// longest).  All sums are fp32; p is rounded to bf16 once, as the matrix unit's
+// operand of the product with v (outputs 2.2-2.3e-3 off, 1.7e-3 from their own
+// rounding alone); the splits' partial outputs stay fp32.
 #include "attn_common.hpp"
 #include "hybrid.hpp"
 
@@ -410,17 +412,28 @@ __global__ __launch_bounds__(256) void attn_join_kernel(CachedArgs a) {
 }
 
 // The direct form where a workgroup per (sequence, head) covers all keys in two
-// rounds of its waves and the card holds them all at once (one sequence, 32 / 8
-// heads of 64, prefix 500, suffix 37: 6.0 us, split 7.1; at 1000 + 100 keys 7.6
-// and 7.5; 64 sequences of 64 keys: 8.0 and 4.8).
+// rounds of its waves and the card holds them all at once.  us in a graph, direct /
+// split, 32 / 8 heads of 64: one sequence, prefix 500, suffix 37: 6.1 / 6.9; 32
+// sequences 6.5 / 8.2; without a prefix 250 keys 4.5 / 6.6, 1000 keys 7.2 / 6.8 (32
+// sequences 9.8 / 13.3).  Up to 128 keys without a prefix the split form is one
+// launch too and 0.4 us faster (64 keys 4.1 / 3.8).  128-wide heads the same way
+// (40 / 8, 250 keys: 5.9 / 7.8).
 //
 // Splits of the split form: the prefix gets workgroups of at least 64 keys, one
 // per CU where the suffixes' bytes take longer than the prefix's products (the
 // rest of the CU reads suffixes meanwhile), two where they do not; the suffixes
 // as many of at least a tile per wave as two rounds of 512 hold.  Measured with
-// 1 / 2 / 4 prefix workgroups per CU: 256 sequences, 4096 + 600 keys, 32 / 8 heads
-// of 64: 59 / 64 / 74 us; 64 x 8 rows, 16384 + 999 keys: 206 / 129 / 121 us, with 40
-// / 8 heads of 128: 524 / 241 / 251 us.
+// 1 / 2 / 4 prefix workgroups per CU (* the rule's), us: 256 x 1 rows, 4096 + 600
+// keys, 32 / 8 heads of 64: 54* / 59 / 67, of 128: 93* / 107 / 125; 64 x 8 rows, 2000 +
+// 2000 keys: 57* / 63 / 72; 16384 + 999 keys: 141 / 117* / 110, with 40 / 8 heads of 128:
+// 360 / 225* / 236; 16 x 4 rows, 32768 + 500: 42 / 40* / 46.  Four gain only in the one
+// of these shapes.
+//
+// Lengths are device data, so the plan takes the page table's width for the
+// suffixes' length.  A table much wider than the sequences costs a small batch the
+// direct form and fills its splits with nothing (one sequence of 500 + 37 keys: a
+// table of 3 pages of 16 6.1 us, 256 pages 8.0, 2048 pages 13.6); 64 and 256
+// sequences measure the same at any width.
 CachedPlan cached_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_keys) {
     CachedPlan p;
     const int G = Hq / Hkv;

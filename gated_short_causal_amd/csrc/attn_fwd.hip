@@ -9,8 +9,14 @@
 // P^T = exp(S^T - m), rounded to bf16, is in place as the operand of
 // O^T += V^T P^T.  P never leaves the registers.
 //
+// Fewer bits: the matrix unit takes bf16 operands, so p enters the product with v
+// rounded once (half a step, 2^-9 of it; l sums the unrounded p).  The output is
+// then off by 2.0e-3 (relative 2-norm, 64-bit softmax) where its own rounding
+// alone gives 1.6e-3; p as the sum of two bf16 parts would cost a third product.
+// Scores, m, l and o stay fp32.
+//
 // What bounds it: long prompts run at the clock that the matrix and vector units
-// leave each other (1.9 GHz of 2.4): T = 8192, 32 / 8 heads of 64, 280 us = 980
+// leave each other (1.9 GHz of 2.4): T = 8192, 32 / 8 heads of 64, 280-290 us = 950-980
 // TFLOP/s with the vector unit busy 76% and the matrix unit 50% of the cycles;
 // 16 / 2 heads of 128, 260-270 us = 1.03 PFLOP/s (a library product of 8192^3:
 // 1.24).  One sequence of up to ~2000 tokens has fewer workgroups than CUs or not

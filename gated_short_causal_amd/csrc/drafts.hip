@@ -272,7 +272,7 @@ __device__ __forceinline__ int find_token(const Source<E>& src, int first, int l
 // LDS.  The wave in whose run the border lies adds its groups' sums up over the
 // lanes, finds the group, then the piece in it, which it reads again.  N: pieces
 // whose loads are in flight at once (at most 64 registers of them: 256 KiB per
-// workgroup).
+// workgroup; with draft rows in fp32, 21 of the sums' registers go to scratch).
 constexpr int kWW = 16;
 constexpr int kWholeGroups = 8;
 template <typename E> constexpr int kWholeN = sizeof(E) == 2 ? 8 : 4;
@@ -401,9 +401,13 @@ int draft_chunks(int V) { return (V + kDraftChunk - 1) / kDraftChunk; }
 
 template <typename E>
 hipError_t launch_drafts(const DraftArgs<E>& a, hipStream_t s) {
-    // split form: few sequences (CUs left idle by one workgroup each) of long rows; us in a graph, whole / split, fp32
-    // with draft rows: 1 x 65536 9.7 / 9.0, 1 x 128256 13.9 / 9.0, 32 x 128256 18.8 / 15.4, 64 x 128256 22.6 / 20.9,
-    // 64 x 65536 13.2 / 15.4, 256 x 65536 26.6 / 34.0
+    // split form: few sequences (CUs left idle by one workgroup each) of long rows.  us in a graph, whole / split, by
+    // sequences and vocabulary; fp32 with draft rows: 1 x 100003 15.0 / 9.1, 32 x 128256 18.9 / 15.5, 64 x 128256 22-24 / 21,
+    // 64 x 65536 13.2 / 15.5, 256 x 65536 27.7 / 33.8; bf16 with: 8 x 100003 22.4 / 10.2, 32 x 128256 17.2 / 13.6, 64 x 128256
+    // 17.3 / 18.2; bf16 without: 1 x 128256 14.5 / 9.8, 32 x 128256 15.3 / 12.2, 64 x 128256 16.3 / 16.4, 256 x 128256 19.8 / 35;
+    // fp32 without: 32 x 128256 15.3 / 13.2, 64 x 128256 15.8 / 17.6.  At 65536 they differ by little up to 32 sequences (1:
+    // 9.6 / 9.1; bf16 11 / 9.3).  The whole form loses where 64 rows of an odd length above 65536 have draft rows in bf16
+    // (64 x 100003: 23.9 / 16.1).
     constexpr int N = kWholeN<E>;
     const bool split = a.V > kWW * kWholeGroups * N * 512 || (a.N <= 32 && a.V > 65536);
     if (!split) {

@@ -36,8 +36,10 @@
  *    page_size are below 2^30.
  *  - An infinity or NaN in k or v of a token reaches the rows that see the token,
  *    and may reach earlier rows of the same sequence within 127 tokens of it
- *    (their probability of it is 0, but 0 * infinity is not).  It reaches no
- *    other sequence.
+ *    (their probability of it is 0, but 0 * infinity is not; over a cache, any
+ *    earlier row of the sequence's L).  One in q, out or d_out of a row reaches
+ *    dk and dv of the keys that the row sees, and may reach those of later keys
+ *    within 127 tokens.  It reaches no other sequence.
  */
 #ifndef LFM2SC_HYBRID_H
 #define LFM2SC_HYBRID_H
