@@ -28,6 +28,12 @@ from .hybrid import (  # noqa: F401
     lfm2sc_attn_backward,
     lfm2sc_attn_backward_workspace_bytes,
     lfm2sc_attn_cached,
+    lfm2sc_attn_cached8,
+    lfm2sc_attn_cached8_workspace_bytes,
     lfm2sc_attn_cached_workspace_bytes,
     lfm2sc_attn_prefill,
+    lfm2sc_cache8_read,
+    lfm2sc_cache8_write,
+    lfm2sc_rotary,
+    lfm2sc_rotary_freqs,
 )

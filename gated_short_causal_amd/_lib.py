@@ -44,6 +44,7 @@ SIGNATURES = {
 
 # the same for include/lfm2sc_hybrid.h
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 HYBRID_SIGNATURES = {
     "lfm2sc_attn_prefill": (_int, [_int, _int, _int, _int, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _vp, _int, _f32, _vp,
                                    _i64, _vp, _vp]),
@@ -53,6 +54,16 @@ HYBRID_SIGNATURES = {
     "lfm2sc_attn_cached_workspace_bytes": (_size, [_int, _int, _int, _int, _int, _int, _int, _int, _int]),
     "lfm2sc_attn_cached": (_int, [_int, _int, _int, _int, _vp, _i64, _int, _int, _vp, _vp, _i64, _int, _int, _vp, _int,
                                   _vp, _int, _vp, _f32, _vp, _i64, _vp, _size, _vp]),
+    "lfm2sc_rotary_freqs": (_int, [_int, _f64, _int, _f64, _f64, _f64, _f64, _vp]),
+    "lfm2sc_rotary": (_int, [_int, _int, _int, _int, _int, _vp, _i64, _vp, _i64, _int, _vp, _i64, _vp, _i64, _int, _i64, _vp,
+                             _vp, _int, _vp, _f32, _vp]),
+    "lfm2sc_cache8_write": (_int, [_int, _int, _int, _int, _vp, _i64, _vp, _i64, _i64, _vp, _int, _vp, _vp, _i64, _vp, _vp, _i64,
+                                   _int, _int, _int, _vp, _int, _vp, _vp]),
+    "lfm2sc_cache8_read": (_int, [_int, _int, _int, _int, _vp, _vp, _i64, _vp, _vp, _i64, _int, _int, _int, _vp, _int, _vp, _vp,
+                                  _i64, _vp, _i64, _i64, _vp, _int, _vp]),
+    "lfm2sc_attn_cached8_workspace_bytes": (_size, [_int, _int, _int, _int, _int, _int, _int, _int]),
+    "lfm2sc_attn_cached8": (_int, [_int, _int, _int, _int, _int, _vp, _i64, _int, _int, _vp, _vp, _i64, _vp, _vp, _i64, _int, _int,
+                                   _int, _vp, _int, _vp, _int, _vp, _int, _f32, _vp, _i64, _vp, _size, _vp]),
     "lfm2sc_accept_drafts_workspace_bytes": (_size, [_int, _int, _int]),
     "lfm2sc_accept_drafts": (_int, [_int, _int, _int, _int, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                     _size, _vp]),

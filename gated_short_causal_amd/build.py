@@ -16,7 +16,9 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblfm2sc.so")
 SOURCES = ["fwd.hip", "bwd.hip", "fused.hip", "fused_split.hip", "interop.hip", "check.hip", "noalloc.hip", "api.cpp",
-           "attn_fwd.hip", "attn_bwd.hip", "attn_cached.hip", "drafts.hip", "api_hybrid.cpp"]
+           "attn_fwd.hip", "attn_bwd.hip", "attn_cached.hip", "drafts.hip", "api_hybrid.cpp",
+           "rotary.hip", "cache8.hip", "attn_cached8.hip", "attn_cached8_e4m3_64.hip", "attn_cached8_e4m3_128.hip",
+           "attn_cached8_int8_64.hip", "attn_cached8_int8_128.hip"]
 
 
 def hipcc() -> str:

@@ -470,6 +470,14 @@ CachedPlan cached_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int
     return p;
 }
 
+hipError_t launch_attn_join(const CachedArgs& a, int D, hipStream_t s) {
+    const int64_t joins = ((int64_t)a.N * a.L * a.Hq + 3) / 4;
+    if (too_many(joins, 256)) return hipErrorInvalidConfiguration;
+    if (D == 64) hipLaunchKernelGGL((attn_join_kernel<64>), dim3((uint32_t)joins), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((attn_join_kernel<128>), dim3((uint32_t)joins), dim3(256), 0, s, a);
+    return hipGetLastError();
+}
+
 template <int D>
 static hipError_t launch_cached(const CachedArgs& a, const CachedPlan& p, hipStream_t s) {
     const int64_t blocks = p.prefix_blocks + p.suffix_blocks;

@@ -1,11 +1,13 @@
-"""Python binding of include/lfm2sc_hybrid.h: attention over packed prompts and over a paged cache, and draft
-verification, in the manner of ``binding``: the C entry points' names, torch tensors in, caller-owned outputs
+"""Python binding of include/lfm2sc_hybrid.h: attention over packed prompts and over a paged cache (bf16, or 8-bit codes
+that are quantised as they are written), rotary positions, and draft verification, in the manner of ``binding``: the C entry points' names, torch tensors in, caller-owned outputs
 written in place on the current stream, and checks of everything visible in the tensors before any library call.
 
 Tensor conventions (see the header for the full contract):
   q, out, gradients  [rows, >= heads*D]  bf16, unit column stride; the number of heads is the width over D
   k, v               [rows, kv_heads*D]
   k_pages, v_pages   [pages, page_size, kv_heads, D] bf16, the last two dense, pages evenly spaced
+  8-bit pages        k [pages, kv_heads, page_size, D], v [pages, kv_heads, page_size/16, D, 16], float8_e4m3fn or int8, dense
+                     within a page; scales [pages, kv_heads, page_size/scale_tokens] fp32
   target_probs       [N*(L+1), V], draft_probs [N*L, V], bf16 or fp32
 """
 import torch
@@ -203,3 +205,148 @@ def lfm2sc_accept_drafts(target_probs, draft_tokens, u_accept, u_sample, accept_
     if rc:
         _check(rc)
     return accept_len, next_token
+
+
+_ROPE = {"plain": 0, "linear": 1, "base": 2, "parts": 3}
+
+
+def lfm2sc_rotary_freqs(rotary_dim, base=10000.0, scaling="plain", factor=1.0, original_len=0.0, low=1.0, high=4.0):
+    """The [rotary_dim / 2] fp32 frequencies (a CPU tensor) that lfm2sc_rotary takes: base^(-2i / rotary_dim), scaled for longer
+    contexts by "linear" (over factor), "base" (base grows) or "parts" (pairs that turn fewer than low times over original_len
+    tokens are slowed by factor, those above high stay)."""
+    if scaling not in _ROPE:
+        raise ValueError(f"scaling must be one of {', '.join(_ROPE)}, got {scaling!r:.100}")
+    freqs = torch.empty(max(0, rotary_dim // 2), dtype=_F32)
+    rc = _lib.hybrid_lib().lfm2sc_rotary_freqs(rotary_dim, base, _ROPE[scaling], factor, original_len, low, high, freqs.data_ptr())
+    if rc:
+        _check(rc)
+    return freqs
+
+
+def lfm2sc_rotary(q, q_out, D, freqs, positions=None, cu_seqlens=None, k=None, k_out=None, interleaved=False, inverse=False,
+                  magnitude=1.0):
+    """Rotary positions of the rows of q [T, heads*D] and, when given, k [T, kv_heads*D]: the first 2 * len(freqs) columns of
+    every head turn by position * freqs.  positions [T]; or with cu_seqlens [N+1] the position of each sequence's first row [N]
+    (None: 0).  q_out may be q and k_out k.  inverse=True: the gradient.  float32 or bfloat16."""
+    dev = _gpu(q, "q")
+    dtype = q.dtype
+    code = _dtype_code(q)
+    T = q.shape[0]
+    Hq = _heads(q_out.shape[-1], D, "q_out")
+    qs, qos = _mat(q, "q", dev, dtype, T, Hq * D), _mat(q_out, "q_out", dev, dtype, T, Hq * D)
+    if (k is None) != (k_out is None):
+        raise ValueError("k and k_out go together")
+    if k is None:
+        Hkv, kp, ks, kop, kos = 0, None, 0, None, 0
+    else:
+        Hkv = _heads(k_out.shape[-1], D, "k_out")
+        kp, ks = k.data_ptr(), _mat(k, "k", dev, dtype, T, Hkv * D)
+        kop, kos = k_out.data_ptr(), _mat(k_out, "k_out", dev, dtype, T, Hkv * D)
+    if cu_seqlens is None:
+        N, cu, pos = 0, None, _needed(positions, "positions", dev, _I32, T)
+    else:
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be a 1-D int32 tensor of N+1 row offsets")
+        N = cu_seqlens.numel() - 1
+        cu, pos = _vec(cu_seqlens, "cu_seqlens", dev, _I32, 1), _vec(positions, "positions", dev, _I32, N)
+    rc = _lib.hybrid_lib().lfm2sc_rotary(
+        code, D, 2 * freqs.numel(), int(interleaved), int(inverse), q.data_ptr(), qs, q_out.data_ptr(), qos, Hq, kp, ks, kop, kos,
+        Hkv, T, pos, cu, N, _vec(freqs, "freqs", dev, _F32, 1), magnitude, binding._stream(q.device))
+    if rc:
+        _check(rc)
+    return q_out if k is None else (q_out, k_out)
+
+
+_FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}
+
+
+def _pool8(k_pages, v_pages, k_scales, v_scales, dev):
+    """(D, kv_heads, addresses and strides of the pools, pages, page_size, scale_tokens, format) of an 8-bit cache."""
+    if k_pages.dtype not in _FORMATS:
+        raise TypeError(f"k_pages must be torch.float8_e4m3fn or torch.int8, got {k_pages.dtype}")
+    if k_pages.dim() != 4 or k_pages.numel() == 0:
+        raise ValueError(f"k_pages must be a [pages, kv_heads, page_size, D] tensor, got shape {tuple(k_pages.shape)}")
+    P, H, S, D = k_pages.shape
+    if v_pages.shape != (P, H, S // 16, D, 16):
+        raise ValueError(f"v_pages must be [pages, kv_heads, page_size / 16, D, 16] = {(P, H, S // 16, D, 16)}, got "
+                         f"{tuple(v_pages.shape)}")
+    B = k_scales.shape[2] if k_scales.dim() == 3 else 0
+    if k_scales.shape != v_scales.shape or B < 1 or S % B != 0 or k_scales.shape != (P, H, B):
+        raise ValueError(f"k_scales and v_scales must be [pages, kv_heads, page_size / scale_tokens] of {P} pages, {H} heads and "
+                         f"{S} tokens, got {tuple(k_scales.shape)} and {tuple(v_scales.shape)}")
+    for name, t, dtype in (("k_pages", k_pages, k_pages.dtype), ("v_pages", v_pages, k_pages.dtype), ("k_scales", k_scales, _F32),
+                           ("v_scales", v_scales, _F32)):
+        if t.dtype is not dtype or t.get_device() != dev:
+            _refuse(t, name, dev, dtype, "part of the cache")
+        if not t[0].is_contiguous():
+            raise ValueError(f"{name} must be dense within a page, got strides {t.stride()}")
+    ps, ss = (k_pages.stride(0), k_scales.stride(0)) if P > 1 else (H * S * D, H * B)
+    if P > 1 and (v_pages.stride(0) != ps or v_scales.stride(0) != ss):
+        raise ValueError("the pages of k and of v, and their scales, must be evenly spaced alike")
+    return (_FORMATS[k_pages.dtype], D, H,
+            (k_pages.data_ptr(), v_pages.data_ptr(), ps, k_scales.data_ptr(), v_scales.data_ptr(), ss, P, S, S // B))
+
+
+def _rows8(k, v, width, page_table, seq_len, cu_seqlens, dev, names):
+    dtype, T = k.dtype, k.shape[0]
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [N, max_pages]")
+    N, most = page_table.shape
+    if cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.numel() != N + 1):
+        raise ValueError(f"cu_seqlens must be a 1-D int32 tensor of {N + 1} row offsets")
+    rows = (k.data_ptr(), _mat(k, names[0], dev, dtype, T, width), v.data_ptr(), _mat(v, names[1], dev, dtype, T, width), T)
+    return rows, _vec(cu_seqlens, "cu_seqlens", dev, _I32, 1), N, (_vec(page_table, "page_table", dev, _I32, 0), most,
+                                                                   _needed(seq_len, "seq_len", dev, _I32, N))
+
+
+def lfm2sc_cache8_write(k, v, k_pages, v_pages, k_scales, v_scales, page_table, seq_len, cu_seqlens=None):
+    """Quantises the rows of k and v [T, kv_heads*D] (bf16 or fp32) into the 8-bit cache, as the newest tokens of the sequences:
+    seq_len [N] counts them in.  Rows are packed by cu_seqlens [N+1], or T / N to every sequence.  page_table [N, max_pages]."""
+    dev = _gpu(k, "k")
+    fmt, D, H, pool = _pool8(k_pages, v_pages, k_scales, v_scales, dev)
+    rows, cu, N, where = _rows8(k, v, H * D, page_table, seq_len, cu_seqlens, dev, ("k", "v"))
+    rc = _lib.hybrid_lib().lfm2sc_cache8_write(_dtype_code(k), fmt, D, H, *rows, cu, N, *pool, *where, binding._stream(k.device))
+    if rc:
+        _check(rc)
+
+
+def lfm2sc_cache8_read(k_pages, v_pages, k_scales, v_scales, page_table, seq_len, k_out, v_out, cu_seqlens=None):
+    """The values of the sequences' last tokens as rows of k_out and v_out [T, kv_heads*D] (bf16 or fp32), packed as
+    lfm2sc_cache8_write takes them."""
+    dev = _gpu(k_out, "k_out")
+    fmt, D, H, pool = _pool8(k_pages, v_pages, k_scales, v_scales, dev)
+    rows, cu, N, where = _rows8(k_out, v_out, H * D, page_table, seq_len, cu_seqlens, dev, ("k_out", "v_out"))
+    rc = _lib.hybrid_lib().lfm2sc_cache8_read(_dtype_code(k_out), fmt, D, H, *pool, *where, *rows, cu, N,
+                                              binding._stream(k_out.device))
+    if rc:
+        _check(rc)
+    return k_out, v_out
+
+
+def lfm2sc_attn_cached8_workspace_bytes(dtype, D, num_heads, num_kv_heads, num_seqs, L, prefix_len, max_suffix_len) -> int:
+    code = binding._DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
+    return int(_lib.hybrid_lib().lfm2sc_attn_cached8_workspace_bytes(code, D, num_heads, num_kv_heads, num_seqs, L, prefix_len,
+                                                                     max_suffix_len))
+
+
+def lfm2sc_attn_cached8(q, k_pages, v_pages, k_scales, v_scales, prefix_pages, prefix_len, page_table, suffix_len, L, out,
+                        workspace, scale=None, max_suffix_len=None):
+    """lfm2sc_attn_cached over the 8-bit cache.  max_suffix_len: the caller's bound on suffix_len (None: what page_table holds);
+    the workspace is asked for with the same."""
+    dev = _gpu(q, "q")
+    dtype = q.dtype
+    fmt, D, H, pool = _pool8(k_pages, v_pages, k_scales, v_scales, dev)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [N, max_pages]")
+    N, most = page_table.shape
+    S = pool[7]
+    prefix = _needed(prefix_pages, "prefix_pages", dev, _I32, -(-prefix_len // S)) if prefix_len > 0 else None
+    Hq = _heads(out.shape[-1], D, "out")
+    rc = _lib.hybrid_lib().lfm2sc_attn_cached8(
+        _dtype_code(q), fmt, D, Hq, H, q.data_ptr(), _mat(q, "q", dev, dtype, N * L, Hq * D), N, L, *pool, prefix, prefix_len,
+        _vec(page_table, "page_table", dev, _I32, 0), most, _needed(suffix_len, "suffix_len", dev, _I32, N),
+        most * S if max_suffix_len is None else max_suffix_len, D ** -0.5 if scale is None else scale, out.data_ptr(),
+        _mat(out, "out", dev, dtype, N * L, Hq * D), *_workspace(workspace, dev), binding._stream(q.device))
+    if rc:
+        _check(rc)
+    return out

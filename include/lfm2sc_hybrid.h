@@ -8,7 +8,12 @@
  *        the block of lfm2sc_verify_window -- over a paged key/value cache whose
  *        first keys are a prefix shared by the whole batch;
  *   lfm2sc_accept_drafts  verification of drafted tokens; its keep_len is the
- *        accept_len that lfm2sc_commit_window takes.
+ *        accept_len that lfm2sc_commit_window takes;
+ *   lfm2sc_rotary         rotary positions of q and k rows, and the gradient, with
+ *        lfm2sc_rotary_freqs for the frequencies;
+ *   lfm2sc_cache8_write / lfm2sc_cache8_read   k and v rows quantised into a paged
+ *        cache of 8-bit codes, and read back;
+ *   lfm2sc_attn_cached8   lfm2sc_attn_cached over that cache.
  *
  * The conventions of lfm2sc.h hold: device pointers owned by the caller, no
  * device memory allocated, asynchronous on `stream`, row-major layouts with
@@ -176,6 +181,156 @@ int lfm2sc_accept_drafts(int dtype, int V, int num_seqs, int L,
                          const float* u_accept, const float* u_sample,
                          int32_t* accept_len, int32_t* keep_len, int32_t* next_token,
                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions.  Passage: MAX LFM2 attention layers (A22 of the hybrid
+ * decoders' draft models: both pairings); the rotation is the published one.
+ */
+
+/* Frequencies for longer contexts than the model was trained on. */
+enum {
+    LFM2SC_ROPE_PLAIN = 0,    /* f_i = base^(-2i / R) */
+    LFM2SC_ROPE_LINEAR = 1,   /* f_i / factor */
+    LFM2SC_ROPE_BASE = 2,     /* base grows by factor^(R / (R - 2)); R >= 4 */
+    LFM2SC_ROPE_PARTS = 3     /* by the turns r_i = original_len f_i / 2 pi that a pair makes over the trained length:
+                                 w = clamp((r_i - low) / (high - low), 0, 1), f_i (w + (1 - w) / factor) */
+};
+
+/*
+ * Fills freqs, HOST memory [R / 2], with the frequencies of R = rotary_dim rotated
+ * columns, worked out in fp64 and rounded once.  base > 1; factor >= 1 (not for
+ * PLAIN); original_len > 0 and 0 <= low < high for PARTS (usual: 1 and 4, or 1 and
+ * 32 with a `magnitude` of 0.1 ln factor + 1).  What a scaling does not use may be 0.
+ */
+int lfm2sc_rotary_freqs(int rotary_dim, double base, int scaling, double factor, double original_len, double low,
+                        double high, float* freqs);
+
+/*
+ * Rotates the first rotary_dim = R columns of every head of q and k; the others
+ * stay.  With angle a = position * freqs[i], a pair (x, y) of a head's columns
+ * becomes
+ *   magnitude * (x cos a - y sin a, y cos a + x sin a);   inverse != 0: sin a -> -sin a,
+ * the gradient of the call with respect to its rows.  Pairs are columns i and
+ * i + R / 2 (interleaved 0), or 2 i and 2 i + 1 (interleaved 1).
+ *
+ * dtype        LFM2SC_BF16 or LFM2SC_F32, of the rows.  Angles are reduced in fp64
+ *              (below 2^24 positions exact to 1e-8 of a turn, up to 2^31 to 1e-6),
+ *              the rotation is fp32, a result is rounded once.
+ * D            a multiple of 8 up to 512; R even, 2 <= R <= D.
+ * q            [total_T][q_stride], num_heads heads of D columns; q_out the same.
+ *              q_out may be q (with the same stride); otherwise the two do not
+ *              overlap.  Strides as for attention: multiples of 8, below 2^22;
+ *              pointers 16-byte aligned.
+ * k, k_out     the same with num_kv_heads heads; with num_kv_heads 0 they are not
+ *              used.
+ * positions    int32.  cu_seqlens NULL: [total_T], the rows' positions.  Otherwise
+ *              rows are packed sequences (offsets as for lfm2sc_prefill_ragged), row
+ *              t of sequence i has position positions[i] + t - cu[i]; positions is
+ *              [num_seqs], or NULL for 0.  Rows of no sequence are not written.
+ * freqs        [R / 2] fp32, device memory.
+ */
+int lfm2sc_rotary(int dtype, int D, int rotary_dim, int interleaved, int inverse,
+                  const void* q, int64_t q_stride, void* q_out, int64_t q_out_stride, int num_heads,
+                  const void* k, int64_t k_stride, void* k_out, int64_t k_out_stride, int num_kv_heads,
+                  int64_t total_T, const int32_t* positions, const int32_t* cu_seqlens, int num_seqs,
+                  const float* freqs, float magnitude, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The cache of 8-bit codes.
+ *
+ * Page p of the pools (uint8 codes, page_stride bytes apart, 16-byte aligned, a
+ * multiple of 16, at least num_kv_heads * page_size * D) holds page_size tokens,
+ * page_size a power of two of at least 16:
+ *   k_pages   [num_kv_heads][page_size][D]
+ *   v_pages   [num_kv_heads][page_size / 16][D][16]: 16 tokens of a channel are neighbours
+ * and its scales (fp32, scale_stride elements apart, at least num_kv_heads *
+ * page_size / scale_tokens)
+ *   k_scales, v_scales [num_kv_heads][page_size / scale_tokens]
+ * with scale_tokens 1, or a power of two of 16 to 128 up to page_size.  A value is
+ * its code times the scale of its head's block of scale_tokens tokens.
+ *
+ * Codes: LFM2SC_CACHE_E4M3 (1.4.3 floats, largest 448) or LFM2SC_CACHE_INT8 (-127 to
+ * 127).  D is 64 or 128.  num_pages * page_size < 2^31.
+ */
+enum { LFM2SC_CACHE_E4M3 = 0, LFM2SC_CACHE_INT8 = 1 };
+
+/*
+ * Writes k and v rows (dtype LFM2SC_BF16 or LFM2SC_F32) as the newest tokens of their
+ * sequences.
+ *
+ * k, v         [total_T][*_stride], num_kv_heads heads of D columns; strides as for
+ *              attention.  Packed sequences by cu_seqlens; or, with cu_seqlens NULL,
+ *              total_T / num_seqs rows of every sequence (the rows of a decode step or
+ *              a verify block; total_T is a multiple of num_seqs).
+ * seq_len      [num_seqs] int32: tokens of the sequence after the call, clamped to
+ *              [0, max_pages * page_size]: its n rows are tokens seq_len - n to
+ *              seq_len - 1 (a row that would come before token 0 is left out).
+ * page_table   [num_seqs][max_pages] int32.  Nothing is written to a page whose number
+ *              is outside [0, num_pages).  No two sequences of a call may write to one
+ *              page.
+ * A block's scale, from the magnitudes of the rows alone that join it (infinities and
+ * NaN apart): where the block holds no earlier token, for INT8 the largest magnitude /
+ * 127 and for E4M3 the lowest power of two s with magnitudes <= 448 s (both at least
+ * 2^-120; 0 if all are 0); where it does (tokens before seq_len - n), the old scale
+ * times the lowest power of two >= 1 that holds the rows (codes up to 127.5 before
+ * rounding, or 448), and the earlier codes are rounded again in steps of the new one,
+ * so that a value stays within one step, however many rows follow.  (An old scale of
+ * 0 or below 2^-120, or 2^40 times too small, makes a new one and zeros of the earlier codes.)
+ * A code is x * (1 / s) rounded to nearest even; beyond the largest it is the largest
+ * (infinities too), a NaN is NaN (E4M3) or 0 (INT8).
+ * In the blocks that the call touches, codes of tokens from seq_len on are not values
+ * of anything; they keep their bits, and tell nothing under a new scale.
+ */
+int lfm2sc_cache8_write(int dtype, int format, int D, int num_kv_heads,
+                        const void* k, int64_t k_stride, const void* v, int64_t v_stride, int64_t total_T,
+                        const int32_t* cu_seqlens, int num_seqs,
+                        void* k_pages, void* v_pages, int64_t page_stride,
+                        float* k_scales, float* v_scales, int64_t scale_stride,
+                        int num_pages, int page_size, int scale_tokens,
+                        const int32_t* page_table, int max_pages, const int32_t* seq_len, void* stream);
+
+/*
+ * The other way round: row t of sequence i receives the value of token seq_len[i] - n
+ * + t, rounded to dtype; a row before token 0 is not written.  Page numbers outside the
+ * pool read as the nearest page.  k_out and v_out [total_T][*_stride].
+ */
+int lfm2sc_cache8_read(int dtype, int format, int D, int num_kv_heads,
+                       const void* k_pages, const void* v_pages, int64_t page_stride,
+                       const float* k_scales, const float* v_scales, int64_t scale_stride,
+                       int num_pages, int page_size, int scale_tokens,
+                       const int32_t* page_table, int max_pages, const int32_t* seq_len,
+                       void* k_out, int64_t k_stride, void* v_out, int64_t v_stride, int64_t total_T,
+                       const int32_t* cu_seqlens, int num_seqs, void* stream);
+
+/*
+ * Bytes of workspace lfm2sc_attn_cached8 needs; 0 for invalid sizes, when num_seqs or L
+ * is 0, and for few keys, which need none.
+ */
+size_t lfm2sc_attn_cached8_workspace_bytes(int dtype, int D, int num_heads, int num_kv_heads, int num_seqs, int L,
+                                           int prefix_len, int max_suffix_len);
+
+/*
+ * lfm2sc_attn_cached over the cache of 8-bit codes: same queries (LFM2SC_BF16), prefix,
+ * page table, lengths, output and workspace rules.  Scores are scale * k_scale * (q .
+ * code); the probability times the value's scale is rounded to bf16 as an operand of
+ * the second product; everything else is fp32.
+ *
+ * max_suffix_len  a bound of the caller's on suffix_len, at most max_pages * page_size
+ *              (suffix_len is clamped to it): the work is split by it, so one near the
+ *              longest sequence serves a wide page table best.
+ * Codes and scales of tokens from a sequence's length on may hold anything.  A NaN code
+ * or an infinite or NaN scale of a token reaches the rows that see it and may reach the
+ * other rows of its sequence's L.
+ */
+int lfm2sc_attn_cached8(int dtype, int format, int D, int num_heads, int num_kv_heads,
+                        const void* q, int64_t q_stride, int num_seqs, int L,
+                        const void* k_pages, const void* v_pages, int64_t page_stride,
+                        const float* k_scales, const float* v_scales, int64_t scale_stride,
+                        int num_pages, int page_size, int scale_tokens,
+                        const int32_t* prefix_pages, int prefix_len,
+                        const int32_t* page_table, int max_pages, const int32_t* suffix_len, int max_suffix_len,
+                        float scale, void* out, int64_t out_stride, void* workspace, size_t workspace_bytes,
+                        void* stream);
 
 #ifdef __cplusplus
 }
