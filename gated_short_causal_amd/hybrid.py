@@ -260,43 +260,59 @@ def lfm2sc_rotary(q, q_out, D, freqs, positions=None, cu_seqlens=None, k=None, k
 _FORMATS = {torch.float8_e4m3fn: 0, torch.int8: 1}
 
 
+def _dense(t, name, inner):
+    """A pool's page stride; a page is dense (strides `inner`, which mean nothing where a size is 1)."""
+    stride = t.stride()
+    if stride[1:] != inner and any(n > 1 and a != b for n, a, b in zip(t.shape[1:], stride[1:], inner)):
+        raise ValueError(f"{name} must be dense within a page, got shape {tuple(t.shape)} strides {stride}")
+    return stride[0]
+
+
 def _pool8(k_pages, v_pages, k_scales, v_scales, dev):
-    """(D, kv_heads, addresses and strides of the pools, pages, page_size, scale_tokens, format) of an 8-bit cache."""
-    if k_pages.dtype not in _FORMATS:
-        raise TypeError(f"k_pages must be torch.float8_e4m3fn or torch.int8, got {k_pages.dtype}")
-    if k_pages.dim() != 4 or k_pages.numel() == 0:
-        raise ValueError(f"k_pages must be a [pages, kv_heads, page_size, D] tensor, got shape {tuple(k_pages.shape)}")
-    P, H, S, D = k_pages.shape
+    """(format, D, kv_heads, (addresses and strides of the pools, pages, page_size, scale_tokens)) of an 8-bit cache."""
+    dtype, shape = k_pages.dtype, k_pages.shape
+    fmt = _FORMATS.get(dtype)
+    if fmt is None:
+        raise TypeError(f"k_pages must be torch.float8_e4m3fn or torch.int8, got {dtype}")
+    if len(shape) != 4 or 0 in shape:
+        raise ValueError(f"k_pages must be a [pages, kv_heads, page_size, D] tensor, got shape {tuple(shape)}")
+    P, H, S, D = shape
     if v_pages.shape != (P, H, S // 16, D, 16):
         raise ValueError(f"v_pages must be [pages, kv_heads, page_size / 16, D, 16] = {(P, H, S // 16, D, 16)}, got "
                          f"{tuple(v_pages.shape)}")
-    B = k_scales.shape[2] if k_scales.dim() == 3 else 0
-    if k_scales.shape != v_scales.shape or B < 1 or S % B != 0 or k_scales.shape != (P, H, B):
+    scales = k_scales.shape
+    B = scales[2] if len(scales) == 3 else 0
+    if B < 1 or S % B != 0 or scales != (P, H, B) or v_scales.shape != scales:
         raise ValueError(f"k_scales and v_scales must be [pages, kv_heads, page_size / scale_tokens] of {P} pages, {H} heads and "
-                         f"{S} tokens, got {tuple(k_scales.shape)} and {tuple(v_scales.shape)}")
-    for name, t, dtype in (("k_pages", k_pages, k_pages.dtype), ("v_pages", v_pages, k_pages.dtype), ("k_scales", k_scales, _F32),
-                           ("v_scales", v_scales, _F32)):
-        if t.dtype is not dtype or t.get_device() != dev:
-            _refuse(t, name, dev, dtype, "part of the cache")
-        if not t[0].is_contiguous():
-            raise ValueError(f"{name} must be dense within a page, got strides {t.stride()}")
-    ps, ss = (k_pages.stride(0), k_scales.stride(0)) if P > 1 else (H * S * D, H * B)
-    if P > 1 and (v_pages.stride(0) != ps or v_scales.stride(0) != ss):
+                         f"{S} tokens, got {tuple(scales)} and {tuple(v_scales.shape)}")
+    for name, t, want in (("k_pages", k_pages, dtype), ("v_pages", v_pages, dtype), ("k_scales", k_scales, _F32),
+                          ("v_scales", v_scales, _F32)):
+        if t.dtype is not want or t.get_device() != dev:
+            _refuse(t, name, dev, want, "part of the cache")
+    page = S * D
+    ps, ss = _dense(k_pages, "k_pages", (page, D, 1)), _dense(k_scales, "k_scales", (B, 1))
+    pv, sv = _dense(v_pages, "v_pages", (page, 16 * D, 16, 1)), _dense(v_scales, "v_scales", (B, 1))
+    if P == 1:
+        ps, ss = H * page, H * B
+    elif pv != ps or sv != ss:
         raise ValueError("the pages of k and of v, and their scales, must be evenly spaced alike")
-    return (_FORMATS[k_pages.dtype], D, H,
-            (k_pages.data_ptr(), v_pages.data_ptr(), ps, k_scales.data_ptr(), v_scales.data_ptr(), ss, P, S, S // B))
+    return fmt, D, H, (k_pages.data_ptr(), v_pages.data_ptr(), ps, k_scales.data_ptr(), v_scales.data_ptr(), ss, P, S, S // B)
 
 
-def _rows8(k, v, width, page_table, seq_len, cu_seqlens, dev, names):
-    dtype, T = k.dtype, k.shape[0]
-    if page_table.dim() != 2:
+def _table(page_table, lens, name, dev):
+    """(N, (page_table's address, max_pages, the lengths' address))"""
+    shape = page_table.shape
+    if len(shape) != 2:
         raise ValueError("page_table must be [N, max_pages]")
-    N, most = page_table.shape
+    return shape[0], (_vec(page_table, "page_table", dev, _I32, 0), shape[1], _needed(lens, name, dev, _I32, shape[0]))
+
+
+def _rows8(k, v, width, cu_seqlens, N, dev, names):
+    dtype, T = k.dtype, k.shape[0]
     if cu_seqlens is not None and (cu_seqlens.dim() != 1 or cu_seqlens.numel() != N + 1):
         raise ValueError(f"cu_seqlens must be a 1-D int32 tensor of {N + 1} row offsets")
-    rows = (k.data_ptr(), _mat(k, names[0], dev, dtype, T, width), v.data_ptr(), _mat(v, names[1], dev, dtype, T, width), T)
-    return rows, _vec(cu_seqlens, "cu_seqlens", dev, _I32, 1), N, (_vec(page_table, "page_table", dev, _I32, 0), most,
-                                                                   _needed(seq_len, "seq_len", dev, _I32, N))
+    return ((k.data_ptr(), _mat(k, names[0], dev, dtype, T, width), v.data_ptr(), _mat(v, names[1], dev, dtype, T, width), T),
+            _vec(cu_seqlens, "cu_seqlens", dev, _I32, 1))
 
 
 def lfm2sc_cache8_write(k, v, k_pages, v_pages, k_scales, v_scales, page_table, seq_len, cu_seqlens=None):
@@ -304,7 +320,8 @@ def lfm2sc_cache8_write(k, v, k_pages, v_pages, k_scales, v_scales, page_table, 
     seq_len [N] counts them in.  Rows are packed by cu_seqlens [N+1], or T / N to every sequence.  page_table [N, max_pages]."""
     dev = _gpu(k, "k")
     fmt, D, H, pool = _pool8(k_pages, v_pages, k_scales, v_scales, dev)
-    rows, cu, N, where = _rows8(k, v, H * D, page_table, seq_len, cu_seqlens, dev, ("k", "v"))
+    N, where = _table(page_table, seq_len, "seq_len", dev)
+    rows, cu = _rows8(k, v, H * D, cu_seqlens, N, dev, ("k", "v"))
     rc = _lib.hybrid_lib().lfm2sc_cache8_write(_dtype_code(k), fmt, D, H, *rows, cu, N, *pool, *where, binding._stream(k.device))
     if rc:
         _check(rc)
@@ -315,7 +332,8 @@ def lfm2sc_cache8_read(k_pages, v_pages, k_scales, v_scales, page_table, seq_len
     lfm2sc_cache8_write takes them."""
     dev = _gpu(k_out, "k_out")
     fmt, D, H, pool = _pool8(k_pages, v_pages, k_scales, v_scales, dev)
-    rows, cu, N, where = _rows8(k_out, v_out, H * D, page_table, seq_len, cu_seqlens, dev, ("k_out", "v_out"))
+    N, where = _table(page_table, seq_len, "seq_len", dev)
+    rows, cu = _rows8(k_out, v_out, H * D, cu_seqlens, N, dev, ("k_out", "v_out"))
     rc = _lib.hybrid_lib().lfm2sc_cache8_read(_dtype_code(k_out), fmt, D, H, *pool, *where, *rows, cu, N,
                                               binding._stream(k_out.device))
     if rc:
@@ -336,16 +354,13 @@ def lfm2sc_attn_cached8(q, k_pages, v_pages, k_scales, v_scales, prefix_pages, p
     dev = _gpu(q, "q")
     dtype = q.dtype
     fmt, D, H, pool = _pool8(k_pages, v_pages, k_scales, v_scales, dev)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [N, max_pages]")
-    N, most = page_table.shape
+    N, (table, most, lens) = _table(page_table, suffix_len, "suffix_len", dev)
     S = pool[7]
     prefix = _needed(prefix_pages, "prefix_pages", dev, _I32, -(-prefix_len // S)) if prefix_len > 0 else None
     Hq = _heads(out.shape[-1], D, "out")
     rc = _lib.hybrid_lib().lfm2sc_attn_cached8(
         _dtype_code(q), fmt, D, Hq, H, q.data_ptr(), _mat(q, "q", dev, dtype, N * L, Hq * D), N, L, *pool, prefix, prefix_len,
-        _vec(page_table, "page_table", dev, _I32, 0), most, _needed(suffix_len, "suffix_len", dev, _I32, N),
-        most * S if max_suffix_len is None else max_suffix_len, D ** -0.5 if scale is None else scale, out.data_ptr(),
+        table, most, lens, most * S if max_suffix_len is None else max_suffix_len, D ** -0.5 if scale is None else scale, out.data_ptr(),
         _mat(out, "out", dev, dtype, N * L, Hq * D), *_workspace(workspace, dev), binding._stream(q.device))
     if rc:
         _check(rc)
