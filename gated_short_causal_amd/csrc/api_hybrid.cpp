@@ -102,7 +102,7 @@ size_t cached_bytes(int D, int Hq, int Hkv, int N, int L, int prefix_len, int ma
 }
 
 size_t cached8_bytes(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_suffix) {
-    const CachedPlan p = cached8_plan(D, Hq, Hkv, N, L, prefix_len, max_suffix);
+    const Cached8Plan p = cached8_plan(D, Hq, Hkv, N, L, prefix_len, max_suffix);
     const size_t rows = (size_t)N * (size_t)L * (size_t)Hq * (size_t)(p.prefix_splits + p.suffix_splits);
     return round_up(rows * (size_t)D * 4) + round_up(rows * 8);
 }
@@ -603,7 +603,7 @@ int lfm2sc_attn_cached8(int dtype, int format, int D, int num_heads, int num_kv_
     c.page_table = page_table; c.max_pages = max_pages; c.suffix_len = suffix_len;
     c.scale = scale;
     c.out = static_cast<uint16_t*>(out); c.out_stride = out_stride;
-    const CachedPlan p = cached8_plan(D, num_heads, num_kv_heads, num_seqs, L, prefix_len, max_suffix_len);
+    const Cached8Plan p = cached8_plan(D, num_heads, num_kv_heads, num_seqs, L, prefix_len, max_suffix_len);
     const size_t rows = (size_t)num_seqs * (size_t)L * (size_t)num_heads * (size_t)(p.prefix_splits + p.suffix_splits);
     c.part_o = static_cast<float*>(workspace);
     c.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(rows * (size_t)D * 4));

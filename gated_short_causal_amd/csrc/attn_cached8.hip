@@ -4,51 +4,54 @@
 
 namespace lfm2sc {
 
-// As cached_plan (attn_cached.hip), with tiles of 64 keys.
-CachedPlan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_suffix) {
-    CachedPlan p;
-    const int G = Hq / Hkv, rows_wg = 16 * cached8_row_tiles(L, G);
+Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_suffix) {
+    Cached8Plan p;
+    const int G = Hq / Hkv, rows_unit = 16 * cached8_row_tiles(L, G);
     const int64_t rows = (int64_t)N * L * G;
-    const int64_t row_blocks = (rows + rows_wg - 1) / rows_wg;
-    const int64_t base = (int64_t)N * (((int64_t)L * G + rows_wg - 1) / rows_wg) * Hkv;
+    const int64_t base = (int64_t)N * (((int64_t)L * G + rows_unit - 1) / rows_unit) * Hkv;
+    const int64_t ptiles = ((int64_t)prefix_len + kC8Tile - 1) / kC8Tile, otiles = ((int64_t)max_suffix + kC8Tile - 1) / kC8Tile;
     p.prefix_splits = 0;
     p.prefix_chunk = 0;
     p.prefix_blocks = 0;
-    const int64_t ptiles = ((int64_t)prefix_len + kC8Tile - 1) / kC8Tile, otiles = ((int64_t)max_suffix + kC8Tile - 1) / kC8Tile;
-    p.direct = base <= 256 && ptiles + otiles <= 2 * kC8DirectWaves;
-    if (p.direct) {
+    p.form = base <= 256 && ptiles + otiles <= 2 * form_waves(kDirect8) ? kDirect8
+             : prefix_len > 0 && rows > 64                              ? kShared8
+                                                                        : kSplit8;
+    if (p.form == kDirect8) {
         p.suffix_splits = 0;
         p.suffix_blocks = base;
         return p;
     }
     if (prefix_len > 0) {
-        const int64_t want = 1024 / (row_blocks * Hkv), most = (ptiles + kC8Waves - 1) / kC8Waves;
+        const int64_t rows_wg = p.form == kShared8 ? kSharedRows : rows_unit, row_blocks = (rows + rows_wg - 1) / rows_wg;
+        const int64_t want = (p.form == kShared8 ? 256 : 1024) / (row_blocks * Hkv);
+        const int64_t most = p.form == kShared8 ? (ptiles + 3) / 4 : (ptiles + 3) / 4;
         const int64_t splits = want < 1 ? 1 : want < most ? want : most;
         const int64_t per = (ptiles + splits - 1) / splits;
         p.prefix_chunk = (int)per * kC8Tile;
         p.prefix_splits = (int)((ptiles + per - 1) / per);
         p.prefix_blocks = row_blocks * Hkv * p.prefix_splits;
     }
-    const int64_t most = (otiles + kC8Waves - 1) / kC8Waves, want = 2048 / base;
+    const int64_t most = (otiles + 3) / 4, want = 2048 / base;
     p.suffix_splits = (int)(want < 1 ? 1 : want < most ? want : most);
     if (p.suffix_splits < 1) p.suffix_splits = 1;
-    p.suffix_blocks = base * p.suffix_splits;
+    const int per_wg = form_waves(p.form) / own_waves(p.form);
+    p.suffix_blocks = (base * p.suffix_splits + per_wg - 1) / per_wg;
     return p;
 }
 
 hipError_t launch_attn_cached8(Cached8Args a, int D, bool int8, hipStream_t s) {
     CachedArgs& c = a.c;
-    const CachedPlan p = cached8_plan(D, c.Hq, c.Hkv, c.N, c.L, c.prefix_len, a.max_suffix);
+    const Cached8Plan p = cached8_plan(D, c.Hq, c.Hkv, c.N, c.L, c.prefix_len, a.max_suffix);
     c.prefix_splits = p.prefix_splits;
     c.prefix_chunk = p.prefix_chunk;
     c.prefix_blocks = p.prefix_blocks;
     c.suffix_splits = p.suffix_splits;
     const int64_t blocks = p.prefix_blocks + p.suffix_blocks;
     const bool join = p.prefix_splits + p.suffix_splits > 1;
-    if (too_many(blocks, 64 * (p.direct ? kC8DirectWaves : kC8Waves)) || (join && too_many(((int64_t)c.N * c.L * c.Hq + 3) / 4, 256)))
+    if (too_many(blocks, 64 * form_waves(p.form)) || (join && too_many(((int64_t)c.N * c.L * c.Hq + 3) / 4, 256)))
         return hipErrorInvalidConfiguration;
-    const hipError_t e = D == 64 ? (int8 ? launch_cached8<64, true>(a, p.direct, blocks, s) : launch_cached8<64, false>(a, p.direct, blocks, s))
-                                 : (int8 ? launch_cached8<128, true>(a, p.direct, blocks, s) : launch_cached8<128, false>(a, p.direct, blocks, s));
+    const hipError_t e = D == 64 ? (int8 ? launch_cached8<64, true>(a, p.form, blocks, s) : launch_cached8<64, false>(a, p.form, blocks, s))
+                                 : (int8 ? launch_cached8<128, true>(a, p.form, blocks, s) : launch_cached8<128, false>(a, p.form, blocks, s));
     if (e != hipSuccess || !join) return e;
     return launch_attn_join(c, D, s);
 }

@@ -113,10 +113,26 @@ struct Loader8 {
         return (is_prefix(i) ? s.prefix : s.own)[group_key(i, x) >> a.c.page_shift];
     }
     __device__ __forceinline__ int clamp_page(int32_t p) const { return min(max(p, 0), a.c.num_pages - 1); }
-    __device__ __forceinline__ void load_k(Tile8<D>& t, int i, int32_t pk, int32_t pg) const {
+    // block 0's codes of the lane, and channel c's
+    __device__ __forceinline__ const uint8_t* key_at(int i, int32_t pk) const {
         const int c = lane & 15, g = lane >> 4, S = 1 << a.c.page_shift;
         const int in = group_key(i, c >> 2) & (S - 1);
-        const uint8_t* p = a.k + (int64_t)clamp_page(pk) * a.page_stride + ((int64_t)kvh * S + in + (c & 3)) * D + D / 4 * g;
+        return a.k + (int64_t)clamp_page(pk) * a.page_stride + ((int64_t)kvh * S + in + (c & 3)) * D + D / 4 * g;
+    }
+    __device__ __forceinline__ const uint8_t* value_at(int i, int32_t pg) const {
+        const int c = lane & 15, g = lane >> 4, S = 1 << a.c.page_shift;
+        const int in = group_key(i, g) & (S - 1);
+        return a.v + (int64_t)clamp_page(pg) * a.page_stride + ((int64_t)kvh * S + in) * D + c * 16;
+    }
+    // 16 codes: part h of block b, and 16 tokens of channel 16 b + c
+    __device__ __forceinline__ uint4 load_key(int i, int b, int h, int32_t pk) const {
+        return *reinterpret_cast<const uint4*>(key_at(i, pk) + 4 * b * D + 16 * h);
+    }
+    __device__ __forceinline__ uint4 load_value(int i, int b, int32_t pg) const {
+        return *reinterpret_cast<const uint4*>(value_at(i, pg) + 256 * b);
+    }
+    __device__ __forceinline__ void load_k(Tile8<D>& t, int i, int32_t pk, int32_t pg) const {
+        const uint8_t* p = key_at(i, pk);
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -124,9 +140,7 @@ struct Loader8 {
         t.ks = scale(a.k_scales, i, pg);
     }
     __device__ __forceinline__ void load_v(Tile8<D>& t, int i, int32_t pg) const {
-        const int c = lane & 15, g = lane >> 4, S = 1 << a.c.page_shift;
-        const int in = group_key(i, g) & (S - 1);
-        const uint8_t* p = a.v + (int64_t)clamp_page(pg) * a.page_stride + ((int64_t)kvh * S + in) * D + c * 16;
+        const uint8_t* p = value_at(i, pg);
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) t.v[b] = *reinterpret_cast<const uint4*>(p + b * 256);
         t.vs = scale(a.v_scales, i, pg);
@@ -138,28 +152,133 @@ struct Loader8 {
     }
 };
 
-// Running softmax state of 16 NT query rows (row 16 n + c): reference m, sum l
-// (of the lane's own keys) and output o, relative to 2^m.
-template <int D, int NT>
+// Running softmax state of 16 NT query rows (row 16 n + c): reference m, sum l and
+// output o, relative to 2^m.  kToken: l is the sum of the lane's own keys.  Else l is
+// a result of the matrix unit like o, with a value 1 / vs in place of a channel's
+// code (rows 0 and 1: its two bf16 parts), because p carries vs: the sum costs
+// nothing of the vector unit, which bounds the kernel where many rows share a tile.
+template <int D, int NT, bool kToken>
 struct Rows8 {
-    float m[NT], l[NT];
+    using Sum = std::conditional_t<kToken, float, f32x4>;
+    float m[NT];
+    Sum l[NT];
     f32x4 o[NT][D / 16];
     __device__ void clear() {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n] = kNegInf;
-            l[n] = 0.f;
+            l[n] = Sum{};
 #pragma unroll
             for (int b = 0; b < D / 16; ++b) o[n][b] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
     }
+    // the row's sum, in all of its lanes
+    __device__ __forceinline__ float sum(int n) const {
+        if constexpr (kToken) return sum_groups(l[n]);
+        else return __shfl(l[n][0] + l[n][1], threadIdx.x & 15, 64);
+    }
 };
 
-// One tile against the wave's rows.  masked (uniform): keys numbered seen[n] + 1 and
-// on within the tile are masked, and keys from `end` on do not exist: their codes
-// and scales may be anything.
+// Scales as the kernels take them.  A scale below 2^-100 (0: a block of zeros)
+// counts as 2^-100, so that its logarithm and reciprocal exist; a NaN stays.
+__device__ __forceinline__ float usable(float scale) { return scale < kMinScale ? kMinScale : scale; }
+
+// Keys that do not exist, from `end` on within the tile: no scale, and (e4m3, where
+// they are in registers) zeros for their values' codes: a NaN among them would
+// outlive its probability of 0.
+template <bool kToken>
+__device__ __forceinline__ void drop_scales(float& ks, float& vs, int end, int lane) {
+    if (16 * (lane >> 4) + (kToken ? lane & 15 : 0) >= end) ks = vs = 1.f;
+}
+__device__ __forceinline__ void drop_codes(uint4& v, int have) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int bytes = min(max(have - 4 * w, 0), 4);
+        (&v.x)[w] &= bytes == 4 ? 0xffffffffu : (1u << (8 * bytes)) - 1u;
+    }
+}
+
+// The scales of a tile in a lane: of its keys' scores (times scale log2 e) and
+// values; kToken: of key 16 g + c, else of the 16 keys of g.
+template <bool kToken>
+struct Scales8 {
+    float k, v;
+    float log_v;                 // else: log2 v, and 1 / v as the operand of l
+    bf16x8 one;
+    __device__ __forceinline__ void set(float ks, float vs, float cs, bool masked, int end, int lane) {
+        if (masked) drop_scales<kToken>(ks, vs, end, lane);
+        k = (kToken ? ks : usable(ks)) * cs;
+        v = vs;
+        if constexpr (!kToken) {
+            v = usable(vs);
+            log_v = __builtin_amdgcn_logf(v);
+            const float r = 1.f / v, hi = __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+            const int c = lane & 15;
+            const uint32_t one1 = c < 2 ? Elem<uint16_t>::pack2(c ? r - hi : hi, c ? r - hi : hi) : 0u;
+            one = __builtin_bit_cast(bf16x8, make_uint4(one1, one1, one1, one1));
+        }
+    }
+};
+
+// The scores of a tile, s[t][i] of key 16 g + 4 t + i, become probabilities times
+// their values' scales: the operands p of the second product.  masked (uniform):
+// keys numbered above `seen` within the tile are masked.
+template <int D, int NT, bool kToken>
+__device__ __forceinline__ void softmax8(Rows8<D, NT, kToken>& r, int n, const f32x4 (&s)[4], bf16x8 (&p)[2], const Scales8<kToken>& sc,
+                                         bool masked, int seen, int g) {
+    float x[16];
+    for_keys([&](auto i) {
+        constexpr int e = decltype(i)::value;
+        if constexpr (kToken) x[e] = s[e >> 2][e & 3] * row_lane<e>(sc.k);
+        else x[e] = s[e >> 2][e & 3];
+    });
+    if (masked) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (16 * g + e > seen) x[e] = kNegInf;
+    }
+    float mx = x[0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) mx = fmaxf(mx, x[e]);
+    const float mn = max_groups(kToken ? mx : mx * sc.k);
+    if (__any(mn > r.m[n] + kLazy)) {
+        const float m = fmaxf(r.m[n], mn), alpha = exp2_fast(r.m[n] - (m == kNegInf ? 0.f : m));
+        r.m[n] = m;
+        r.l[n] *= alpha;
+#pragma unroll
+        for (int b = 0; b < D / 16; ++b) r.o[n][b] *= alpha;
+    }
+    const float ref = r.m[n] == kNegInf ? 0.f : r.m[n];
+    if constexpr (kToken) {
+        float sum = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+            x[e] = exp2_fast(x[e] - ref);
+            sum += x[e];
+        }
+        r.l[n] += sum;
+        for_keys([&](auto i) {
+            constexpr int e = decltype(i)::value;
+            x[e] *= row_lane<e>(sc.v);
+        });
+    } else {
+        const float at = sc.log_v - ref;         // p vs = 2^(score - ref + log2 vs)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[e] = exp2_fast(__builtin_fmaf(x[e], sc.k, at));
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        union { uint32_t w[4]; bf16x8 v; } y;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y.w[j] = Elem<uint16_t>::pack2(x[8 * u + 2 * j], x[8 * u + 2 * j + 1]);
+        p[u] = y.v;
+        if constexpr (!kToken) r.l[n] = mfma16(sc.one, y.v, r.l[n]);
+    }
+}
+
+// One tile, in registers, against the wave's rows.
 template <int D, int NT, bool kInt8, bool kToken, typename F1, typename F2>
-__device__ __forceinline__ void attend8(Rows8<D, NT>& r, const bf16x8 (&q)[NT][D / 32], Tile8<D>& t, float cs, bool masked,
+__device__ __forceinline__ void attend8(Rows8<D, NT, kToken>& r, const bf16x8 (&q)[NT][D / 32], Tile8<D>& t, float cs, bool masked,
                                         const int (&seen)[NT], int end, int lane, F1 after_k, F2 after_v) {
     const int g = lane >> 4;
     f32x4 s[NT][4];
@@ -178,71 +297,16 @@ __device__ __forceinline__ void attend8(Rows8<D, NT>& r, const bf16x8 (&q)[NT][D
             for (int d = 0; d < D / 32; ++d) s[n][b] = mfma16(k[d], q[n][d], s[n][b]);
         }
     }
-    float ks = t.ks * cs, vs = t.vs;
+    Scales8<kToken> sc;
+    sc.set(t.ks, t.vs, cs, masked, end, lane);
     after_k();
-    if (masked) {
-        const int at = 16 * g + (kToken ? lane & 15 : 0);
-        if (at >= end) ks = vs = 0.f;
-        if constexpr (!kInt8) {
-            // codes of tokens that do not exist: a NaN among them would outlive its probability of 0
-            const int have = min(max(end - 16 * g, 0), 16);
+    if (!kInt8 && masked) {
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int bytes = min(max(have - 4 * w, 0), 4);
-                const uint32_t m = bytes == 4 ? 0xffffffffu : (1u << (8 * bytes)) - 1u;
-#pragma unroll
-                for (int b = 0; b < D / 16; ++b) (&t.v[b].x)[w] &= m;
-            }
-        }
+        for (int b = 0; b < D / 16; ++b) drop_codes(t.v[b], end - 16 * g);
     }
     bf16x8 p[NT][2];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float x[16];
-        for_keys([&](auto i) {
-            constexpr int e = decltype(i)::value;
-            if constexpr (kToken) x[e] = s[n][e >> 2][e & 3] * row_lane<e>(ks);
-            else x[e] = s[n][e >> 2][e & 3];
-        });
-        if (masked) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (16 * g + e > seen[n]) x[e] = kNegInf;
-        }
-        float mx = x[0];
-#pragma unroll
-        for (int e = 1; e < 16; ++e) mx = fmaxf(mx, x[e]);
-        // a masked lane's scale may be 0, and 0 times -inf is no maximum
-        const float mn = max_groups(kToken ? mx : mx == kNegInf ? kNegInf : mx * ks);
-        if (__any(mn > r.m[n] + kLazy)) {
-            const float m = fmaxf(r.m[n], mn), alpha = exp2_fast(r.m[n] - (m == kNegInf ? 0.f : m));
-            r.m[n] = m;
-            r.l[n] *= alpha;
-#pragma unroll
-            for (int b = 0; b < D / 16; ++b) r.o[n][b] *= alpha;
-        }
-        const float ref = r.m[n] == kNegInf ? 0.f : r.m[n];
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            if constexpr (kToken) x[e] = exp2_fast(x[e] - ref);
-            else x[e] = masked && x[e] == kNegInf ? 0.f : exp2_fast(__builtin_fmaf(x[e], ks, -ref));
-            sum += x[e];
-        }
-        r.l[n] += sum;
-        for_keys([&](auto i) {
-            constexpr int e = decltype(i)::value;
-            if constexpr (kToken) x[e] *= row_lane<e>(vs);
-            else x[e] *= vs;
-        });
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            union { uint32_t w[4]; bf16x8 v; } y;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y.w[j] = Elem<uint16_t>::pack2(x[8 * u + 2 * j], x[8 * u + 2 * j + 1]);
-            p[n][u] = y.v;
-        }
-    }
+    for (int n = 0; n < NT; ++n) softmax8<D, NT, kToken>(r, n, s[n], p[n], sc, masked, seen[n], g);
 #pragma unroll
     for (int b = 0; b < D / 16; ++b) {
         const bf16x8 v0 = codes_to_bf16<kInt8>(t.v[b].x, t.v[b].y), v1 = codes_to_bf16<kInt8>(t.v[b].z, t.v[b].w);
@@ -259,7 +323,7 @@ __device__ __forceinline__ void attend8(Rows8<D, NT>& r, const bf16x8 (&q)[NT][D
 // is loaded as soon as the scores are formed, its V after the products, its page
 // numbers a tile earlier.
 template <int D, int NT, bool kInt8, bool kToken>
-__device__ __forceinline__ void walk8(Rows8<D, NT>& r, const bf16x8 (&q)[NT][D / 32], const Cached8Args& a, const Keys8& s,
+__device__ __forceinline__ void walk8(Rows8<D, NT, kToken>& r, const bf16x8 (&q)[NT][D / 32], const Cached8Args& a, const Keys8& s,
                                       int kvh, int tiles, int mine, int step, const int (&last)[NT], int least, int lane) {
     if (mine >= tiles) return;
     const int c = lane & 15, g = lane >> 4;
@@ -309,38 +373,73 @@ __device__ __forceinline__ void load_query8(bf16x8 (&f)[D / 32], const uint16_t*
     }
 }
 
-// A workgroup: 16 NT query rows of one key/value head against some of the keys.
-// Own keys: rows of one sequence; prefix: rows of any.  The waves deal the tiles
-// out among themselves and join through LDS, in halves.
-template <int D, int NT, bool kInt8, bool kToken, int W>
-__device__ __forceinline__ void keys8(const Cached8Args& a, const Keys8& s, int kvh, int64_t x0, int64_t rows, int len, int tiles,
-                                      int split, bool whole, float* lds, int wave, int lane) {
-    constexpr int kWaveF = NT * (D / 4 + 2) * 64;        // floats of a wave's state
-    const CachedArgs& ca = a.c;
-    const int c = lane & 15, g = lane >> 4, G = ca.Hq / ca.Hkv;
-    int64_t token[NT];
-    int head[NT], last[NT], least = 1 << 30;
-    bool exists[NT];
-    bf16x8 q[NT][D / 32];
+// Query row x of a key/value head: x = (token row) * G + head in the group.
+struct Query8 {
+    int token, head;
+    bool exists;
+};
+__device__ __forceinline__ Query8 query8(const CachedArgs& a, int kvh, int x, int rows) {
+    const int G = a.Hq / a.Hkv, y = max(min(x, rows - 1), 0);
+    return Query8{y / G, kvh * G + y % G, x < rows};
+}
+
+// Writes the output (whole) of the rows x0 + 16 n + c, or their state to split
+// `split` of the workspace.
+template <int D, int NT, bool kToken>
+__device__ __forceinline__ void store8(const CachedArgs& a, const Rows8<D, NT, kToken>& r, const float (&l)[NT], int kvh, int x0,
+                                       int rows, int split, bool whole, int lane) {
+    const int c = lane & 15, g = lane >> 4;
+    asm volatile("" : "+s"(x0));                         // worked out here, not kept in registers through the loop
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int64_t x = min(x0 + 16 * n + c, rows - 1);
-        exists[n] = x0 + 16 * n + c < rows;
-        token[n] = x / G;
-        head[n] = kvh * G + (int)(x % G);
-        last[n] = len - ca.L + (int)(token[n] % ca.L);   // the row's last own key
-        load_query8<D>(q[n], ca.q + token[n] * ca.q_stride + (int64_t)head[n] * D, g, exists[n]);
+        const Query8 y = query8(a, kvh, x0 + 16 * n + c, rows);
+        if (!y.exists) continue;
+        if (whole) {
+            // no visible key: 0; a NaN stays
+            const float inv = l[n] > 0.f ? 1.f / l[n] : (l[n] == 0.f ? 0.f : l[n]);
+            uint16_t* o = a.out + y.token * a.out_stride + y.head * D + 4 * g;
+#pragma unroll
+            for (int b = 0; b < D / 16; ++b)
+                *reinterpret_cast<uint2*>(o + 16 * b) =
+                    make_uint2(Elem<uint16_t>::pack2(r.o[n][b][0] * inv, r.o[n][b][1] * inv),
+                               Elem<uint16_t>::pack2(r.o[n][b][2] * inv, r.o[n][b][3] * inv));
+        } else {
+            const int64_t at = ((int64_t)split * a.N * a.L + y.token) * a.Hq + y.head;
+#pragma unroll
+            for (int b = 0; b < D / 16; ++b) *reinterpret_cast<f32x4*>(a.part_o + at * D + 16 * b + 4 * g) = r.o[n][b];
+            if (g == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(r.m[n], l[n]);
+        }
     }
-    least = len - ca.L;
-    Rows8<D, NT> r;
+}
+
+// U waves: 16 NT query rows of one key/value head against some of the keys.  Own
+// keys: rows of one sequence; prefix: rows of any.  The waves deal the tiles out
+// among themselves and join through LDS, in halves.  All waves of the workgroup
+// come here together.
+template <int D, int NT>
+constexpr int join_floats() { return NT * (D / 4 + 2) * 64; }      // a wave's state
+template <int D, int NT, bool kInt8, bool kToken, int U>
+__device__ __forceinline__ void keys8(const Cached8Args& a, const Keys8& s, int kvh, int x0, int rows, int len, int tiles, int split,
+                                      bool whole, float* lds, int wave, int lane) {
+    const CachedArgs& ca = a.c;
+    bf16x8 q[NT][D / 32];
+    int last[NT];                                        // the row's last own key
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const Query8 y = query8(ca, kvh, x0 + 16 * n + (lane & 15), rows);
+        load_query8<D>(q[n], ca.q + y.token * ca.q_stride + y.head * D, lane >> 4, y.exists);
+        last[n] = len - ca.L + y.token % ca.L;
+    }
+    Rows8<D, NT, kToken> r;
     r.clear();
-    walk8<D, NT, kInt8, kToken>(r, q, a, s, kvh, tiles, wave, W, last, least, lane);
+    walk8<D, NT, kInt8, kToken>(r, q, a, s, kvh, tiles, wave, U, last, len - ca.L, lane);
+    float l[NT];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) r.l[n] = sum_groups(r.l[n]);
+    for (int n = 0; n < NT; ++n) l[n] = r.sum(n);
 #pragma unroll
-    for (int half = W / 2; half >= 1; half >>= 1) {
-        float* mine = lds + (wave % half) * kWaveF;
-        if (half < W / 2) lds_barrier();                 // the last round's states are read
+    for (int half = U / 2; half >= 1; half >>= 1) {
+        float* mine = lds + (wave % half) * join_floats<D, NT>();
+        if (half < U / 2) lds_barrier();                 // the last round's states are read
         if (wave >= half && wave < 2 * half) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
@@ -348,7 +447,7 @@ __device__ __forceinline__ void keys8(const Cached8Args& a, const Keys8& s, int 
                 for (int b = 0; b < D / 16; ++b)
                     *reinterpret_cast<f32x4*>(mine + ((n * (D / 16) + b) * 64 + lane) * 4) = r.o[n][b];
                 mine[NT * D / 4 * 64 + (2 * n) * 64 + lane] = r.m[n];
-                mine[NT * D / 4 * 64 + (2 * n + 1) * 64 + lane] = r.l[n];
+                mine[NT * D / 4 * 64 + (2 * n + 1) * 64 + lane] = l[n];
             }
         }
         lds_barrier();
@@ -359,47 +458,143 @@ __device__ __forceinline__ void keys8(const Cached8Args& a, const Keys8& s, int 
                 const float m = fmaxf(r.m[n], m2), ref = m == kNegInf ? 0.f : m;
                 const float f1 = exp2_fast(r.m[n] - ref), f2 = exp2_fast(m2 - ref);
                 r.m[n] = m;
-                r.l[n] = r.l[n] * f1 + l2 * f2;
+                l[n] = l[n] * f1 + l2 * f2;
 #pragma unroll
                 for (int b = 0; b < D / 16; ++b)
                     r.o[n][b] = r.o[n][b] * f1 + *reinterpret_cast<const f32x4*>(mine + ((n * (D / 16) + b) * 64 + lane) * 4) * f2;
             }
         }
     }
-    if (wave != 0) return;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        if (!exists[n]) continue;
-        if (whole) {
-            // no visible key: 0; a NaN stays
-            const float inv = r.l[n] > 0.f ? 1.f / r.l[n] : (r.l[n] == 0.f ? 0.f : r.l[n]);
-            uint16_t* o = ca.out + token[n] * ca.out_stride + (int64_t)head[n] * D + 4 * g;
-#pragma unroll
-            for (int b = 0; b < D / 16; ++b)
-                *reinterpret_cast<uint2*>(o + 16 * b) =
-                    make_uint2(Elem<uint16_t>::pack2(r.o[n][b][0] * inv, r.o[n][b][1] * inv),
-                               Elem<uint16_t>::pack2(r.o[n][b][2] * inv, r.o[n][b][3] * inv));
-        } else {
-            const int64_t at = ((int64_t)split * ca.N * ca.L + token[n]) * ca.Hq + head[n];
-#pragma unroll
-            for (int b = 0; b < D / 16; ++b) *reinterpret_cast<f32x4*>(ca.part_o + at * D + 16 * b + 4 * g) = r.o[n][b];
-            if (g == 0) *reinterpret_cast<float2*>(ca.part_ml + at * 2) = make_float2(r.m[n], r.l[n]);
-        }
-    }
+    if (wave == 0) store8<D, NT, kToken>(ca, r, l, kvh, x0, rows, split, whole, lane);
 }
 
-// Split form (direct = false): the prefix's workgroups first, then the suffixes'.
-// Direct form: a workgroup reads prefix and suffix and writes the output.
-template <int D, int NT, bool kInt8, bool kToken, int W>
-__global__ __launch_bounds__(64 * W) void attn_cached8_kernel(Cached8Args a, bool direct) {
-    __shared__ __attribute__((aligned(16))) float lds[W / 2 * NT * (D / 4 + 2) * 64];
+// Prefix keys for many rows: 8 waves of 32 query rows share each tile.  They turn
+// its codes into bf16 operands once, in LDS in the order in which the products
+// read them (operand, lane: 16 bytes each, no bank conflict), two buffers, one
+// barrier a tile; the next tile's codes are in registers meanwhile.
+constexpr int kSharedRows = 32 * 8;
+template <int D>
+constexpr int shared_bytes() { return 2 * kC8Tile * D * 2; }       // a buffer: K and V of a tile
+template <int D, bool kInt8, bool kToken>
+__device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, int kvh, int x0, int rows, int split, uint4* lds, int wave,
+                                        int lane) {
+    constexpr int NT = 2, kKey = 4 * (D / 32) * 64, kBuf = shared_bytes<D>() / 16;
+    const CachedArgs& ca = a.c;
+    const int c = lane & 15, g = lane >> 4;
+    x0 += 32 * wave;
+    const bool busy = x0 < rows;
+    bf16x8 q[NT][D / 32];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const Query8 y = query8(ca, kvh, x0 + 16 * n + c, rows);
+        load_query8<D>(q[n], ca.q + y.token * ca.q_stride + y.head * D, g, y.exists);
+    }
+    const Loader8<D, kInt8, kToken> ld{a, s, kvh, lane};
+    const float cs = ca.scale * kLog2e;
+    Rows8<D, NT, kToken> r;
+    r.clear();
+    // D = 128: wave w brings half (w & 1) of the keys' block w >> 1, and channels 16 w ..; D = 64: waves 0 to 3 a block of
+    // keys each, waves 4 to 7 16 channels each.
+    uint4 kc, vc;
+    float ks, vs;
+    auto load = [&](int i, int32_t pk, int32_t pg) {
+        if (D == 128 || wave < 4) kc = ld.load_key(i, D == 128 ? wave >> 1 : wave, D == 128 ? wave & 1 : 0, pk);
+        if (D == 128 || wave >= 4) vc = ld.load_value(i, D == 128 ? wave : wave - 4, pg);
+        ks = ld.scale(a.k_scales, i, pg);
+        vs = ld.scale(a.v_scales, i, pg);
+    };
+    auto stage = [&](uint4* buf, int i) {
+        const int end = ld.end_key(i) - ld.first_key(i);
+        if (D == 128 || wave < 4) {
+            uint4* p = buf + (D == 128 ? (wave >> 1) * 4 + (wave & 1) * 2 : wave * 2) * 64 + lane;
+            p[0] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(kc.x, kc.y));
+            p[64] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(kc.z, kc.w));
+        }
+        if (D == 128 || wave >= 4) {
+            if (!kInt8 && end < kC8Tile) drop_codes(vc, end - 16 * g);
+            uint4* p = buf + kKey + (D == 128 ? wave : wave - 4) * 2 * 64 + lane;
+            p[0] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(vc.x, vc.y));
+            p[64] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(vc.z, vc.w));
+        }
+    };
+    load(0, ld.page(0, c >> 2), ld.page(0, g));
+    int32_t nk = 0, ng = 0;
+    if (s.ptiles > 1) {
+        nk = ld.page(1, c >> 2);
+        ng = ld.page(1, g);
+    }
+    for (int i = 0; i < s.ptiles; ++i) {
+        uint4* buf = lds + (i & 1) * kBuf;
+        stage(buf, i);
+        const int end = ld.end_key(i) - ld.first_key(i);
+        const bool masked = end < kC8Tile;
+        Scales8<kToken> f;
+        f.set(ks, vs, cs, masked, end, lane);
+        if (i + 1 < s.ptiles) {
+            const int32_t pk = nk, pg = ng;
+            const int then = min(i + 2, s.ptiles - 1);
+            nk = ld.page(then, c >> 2);
+            ng = ld.page(then, g);
+            load(i + 1, pk, pg);
+        }
+        lds_barrier();
+        if (!busy) continue;
+        f32x4 sc[NT][4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sc[n][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int d = 0; d < D / 32; ++d) {
+                const bf16x8 k = __builtin_bit_cast(bf16x8, buf[(b * (D / 32) + d) * 64 + lane]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) sc[n][b] = mfma16(k, q[n][d], sc[n][b]);
+            }
+        }
+        bf16x8 p[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) softmax8<D, NT, kToken>(r, n, sc[n], p[n], f, masked, end - 1, g);
+#pragma unroll
+        for (int b = 0; b < D / 16; ++b)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bf16x8 v = __builtin_bit_cast(bf16x8, buf[kKey + (b * 2 + u) * 64 + lane]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) r.o[n][b] = mfma16(v, p[n][u], r.o[n][b]);
+            }
+    }
+    float l[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) l[n] = r.sum(n);
+    if (busy) store8<D, NT, kToken>(ca, r, l, kvh, x0, rows, split, false, lane);
+}
+
+// Forms of a call (see cached8_plan).
+//   kDirect  a workgroup of 8 waves reads prefix and suffix of its rows and writes the output
+//   kSplit   workgroups of 4 waves, the prefix's first (few rows), then the suffixes'
+//   kShared  workgroups of 8 waves: the prefix's (many rows, shared8), then two units of 4 waves of the suffixes
+enum Form8 { kDirect8, kSplit8, kShared8 };
+constexpr int form_waves(int form) { return form == kSplit8 ? 4 : 8; }
+// waves a SIMD, which bounds their registers: 128, 168 or 256 of 512
+constexpr int form_per_simd(int D, int NT, int form) {
+    if (D == 64 && NT == 1) return 4;
+    return form == kSplit8 && (D == 64 || NT == 1) ? 3 : 2;
+}
+constexpr int own_waves(int form) { return form == kDirect8 ? 8 : 4; }
+
+template <int D, int NT, bool kInt8, bool kToken, int kForm>
+__global__ __launch_bounds__(64 * form_waves(kForm), form_per_simd(D, NT, kForm)) void attn_cached8_kernel(Cached8Args a) {
+    constexpr int W = form_waves(kForm), U = own_waves(kForm);
+    constexpr int kJoin = W / 2 * join_floats<D, NT>() * 4;
+    constexpr int kLds = kForm == kShared8 && 2 * shared_bytes<D>() > kJoin ? 2 * shared_bytes<D>() : kJoin;
+    __shared__ uint4 lds[kLds / 16];
     const CachedArgs& ca = a.c;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int G = ca.Hq / ca.Hkv, prefix_blocks = (int)ca.prefix_blocks;
     int block = blockIdx.x;
     Keys8 s;
     s.prefix = ca.prefix_pages;
-    if (block < prefix_blocks) {
+    if (kForm != kDirect8 && block < prefix_blocks) {
         const int kvh = block % ca.Hkv, rest = block / ca.Hkv, split = rest % ca.prefix_splits;
         s.own = nullptr;
         s.len = 0;
@@ -407,60 +602,67 @@ __global__ __launch_bounds__(64 * W) void attn_cached8_kernel(Cached8Args a, boo
         s.p1 = min(s.p0 + ca.prefix_chunk, ca.prefix_len);
         s.ptiles = (s.p1 - s.p0 + kC8Tile - 1) / kC8Tile;
         s.tile0 = 0;
-        keys8<D, NT, kInt8, kToken, W>(a, s, kvh, (int64_t)(rest / ca.prefix_splits) * 16 * NT, (int64_t)ca.N * ca.L * G, 0,
-                                       s.ptiles, split, false, lds, wave, lane);
+        const int rows = ca.N * ca.L * G;
+        if constexpr (kForm == kShared8)
+            shared8<D, kInt8, kToken>(a, s, kvh, rest / ca.prefix_splits * kSharedRows, rows, split, lds, wave, lane);
+        else
+            keys8<D, NT, kInt8, kToken, U>(a, s, kvh, rest / ca.prefix_splits * 16 * NT, rows, 0, s.ptiles, split, false,
+                                           reinterpret_cast<float*>(lds), wave, lane);
         return;
     }
-    block -= prefix_blocks;
-    const int kvh = block % ca.Hkv;
-    int rest = block / ca.Hkv;
-    const int splits = direct ? 1 : ca.suffix_splits, split = rest % splits;
+    const int unit_wave = wave % U;
+    const int64_t units = (int64_t)ca.N * ((ca.L * G + 16 * NT - 1) / (16 * NT)) * ca.Hkv * (kForm == kDirect8 ? 1 : ca.suffix_splits);
+    const int64_t mine = (int64_t)(block - prefix_blocks) * (W / U) + wave / U;
+    const bool none = mine >= units;             // the last workgroup's second unit
+    int rest = (int)(none ? units - 1 : mine);
+    const int kvh = rest % ca.Hkv;
+    rest /= ca.Hkv;
+    const int splits = kForm == kDirect8 ? 1 : ca.suffix_splits, split = rest % splits;
     rest /= splits;
     const int blocks = (ca.L * G + 16 * NT - 1) / (16 * NT);
     const int seq = rest / blocks, rb = rest % blocks;
     s.own = ca.page_table + (int64_t)seq * ca.max_pages;
-    s.len = min(max(ca.suffix_len[seq], 0), a.max_suffix);
+    s.len = none ? 0 : min(max(ca.suffix_len[seq], 0), a.max_suffix);
     s.p0 = 0;
-    s.p1 = direct ? ca.prefix_len : 0;
+    s.p1 = kForm == kDirect8 ? ca.prefix_len : 0;
     s.ptiles = (s.p1 + kC8Tile - 1) / kC8Tile;
     const int all = (s.len + kC8Tile - 1) / kC8Tile, per = (all + splits - 1) / splits;
     const int t0 = min(split * per, all), t1 = min(t0 + per, all);
     s.tile0 = t0;
-    keys8<D, NT, kInt8, kToken, W>(a, s, kvh, (int64_t)seq * ca.L * G + (int64_t)rb * 16 * NT, (int64_t)(seq + 1) * ca.L * G, s.len,
-                                   s.ptiles + t1 - t0, ca.prefix_splits + split, direct || ca.prefix_splits + splits == 1, lds, wave,
-                                   lane);
+    const int end = none ? 0 : (seq + 1) * ca.L * G;        // no row exists for `none`
+    keys8<D, NT, kInt8, kToken, U>(a, s, kvh, seq * ca.L * G + rb * 16 * NT, end, s.len, s.ptiles + t1 - t0,
+                                   ca.prefix_splits + split, kForm == kDirect8 || ca.prefix_splits + splits == 1,
+                                   reinterpret_cast<float*>(lds) + (wave / U) * (U / 2) * join_floats<D, NT>(), unit_wave, lane);
 }
 
-constexpr int kC8Waves = 4, kC8DirectWaves = 8;
 inline int cached8_row_tiles(int L, int G) { return (int64_t)L * G <= 16 ? 1 : 2; }
 
 // Defined in the file of its format and head dimension.
 template <int D, bool kInt8>
-hipError_t launch_cached8(const Cached8Args& a, bool direct, int64_t blocks, hipStream_t s);
+hipError_t launch_cached8(const Cached8Args& a, int form, int64_t blocks, hipStream_t s);
 
 #ifdef LFM2SC_CACHED8_D
 template <int D, bool kInt8>
-hipError_t launch_cached8(const Cached8Args& a, bool direct, int64_t blocks, hipStream_t s) {
-    const int nt = cached8_row_tiles(a.c.L, a.c.Hq / a.c.Hkv);
-    auto go = [&](auto n, auto token) {
-        constexpr int NT = decltype(n)::value;
-        constexpr bool kToken = decltype(token)::value;
-        if (direct)
-            hipLaunchKernelGGL((attn_cached8_kernel<D, NT, kInt8, kToken, kC8DirectWaves>), dim3((uint32_t)blocks),
-                               dim3(64 * kC8DirectWaves), 0, s, a, true);
-        else
-            hipLaunchKernelGGL((attn_cached8_kernel<D, NT, kInt8, kToken, kC8Waves>), dim3((uint32_t)blocks), dim3(64 * kC8Waves), 0,
-                               s, a, false);
+hipError_t launch_cached8(const Cached8Args& a, int form, int64_t blocks, hipStream_t s) {
+    auto go = [&](auto n, auto token, auto f) {
+        constexpr int kForm = decltype(f)::value;
+        hipLaunchKernelGGL((attn_cached8_kernel<D, decltype(n)::value, kInt8, decltype(token)::value, kForm>), dim3((uint32_t)blocks),
+                           dim3(64 * form_waves(kForm)), 0, s, a);
     };
-    auto by_rows = [&](auto token) {
-        if (nt == 1) go(IC<1>{}, token);
-        else go(IC<2>{}, token);
+    auto by_form = [&](auto n, auto token) {
+        if (form == kDirect8) go(n, token, IC<kDirect8>{});
+        else if (form == kSplit8) go(n, token, IC<kSplit8>{});
+        else go(n, token, IC<kShared8>{});
     };
-    if (a.block_shift == 0) by_rows(std::true_type{});
-    else by_rows(std::false_type{});
+    auto by_token = [&](auto n) {
+        if (a.block_shift == 0) by_form(n, std::true_type{});
+        else by_form(n, std::false_type{});
+    };
+    if (cached8_row_tiles(a.c.L, a.c.Hq / a.c.Hkv) == 1) by_token(IC<1>{});
+    else by_token(IC<2>{});
     return hipGetLastError();
 }
-template hipError_t launch_cached8<LFM2SC_CACHED8_D, LFM2SC_CACHED8_INT8>(const Cached8Args&, bool, int64_t, hipStream_t);
+template hipError_t launch_cached8<LFM2SC_CACHED8_D, LFM2SC_CACHED8_INT8>(const Cached8Args&, int, int64_t, hipStream_t);
 #endif
 
 }  // namespace lfm2sc

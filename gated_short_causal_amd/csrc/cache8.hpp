@@ -17,7 +17,7 @@
 namespace lfm2sc {
 
 constexpr int kTileTokens = 16;
-constexpr float kMinScale = 7.52316385e-37f;     // 2^-120: its reciprocal is finite
+constexpr float kMinScale = 7.88860905e-31f;     // 2^-100: its reciprocal, and products with it, are normal numbers
 
 template <bool kInt8>
 __device__ __forceinline__ float code_max() { return kInt8 ? 127.f : 448.f; }
@@ -77,7 +77,7 @@ __device__ __forceinline__ float fresh_scale(float top) {
     if constexpr (kInt8) return fmaxf(top / 127.f, kMinScale);
     const uint32_t b = __float_as_uint(top);     // 448 = 1.75 * 2^8
     const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u ? 1 : 0);
-    return __uint_as_float((uint32_t)(e < 7 ? 7 : e) << 23);       // 2^-120 or more
+    return __uint_as_float((uint32_t)(e < 27 ? 27 : e) << 23);     // 2^-100 or more
 }
 
 // The scale of a block that keeps tokens of scale `old` when new ones of largest

@@ -116,7 +116,12 @@ struct Cached8Args {
     int block_shift;
     int max_suffix;                              // longest suffix, in keys
 };
-CachedPlan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_suffix);
+struct Cached8Plan {
+    int form;                            // Form8 (attn_cached8.hpp)
+    int prefix_splits, prefix_chunk, suffix_splits;
+    int64_t prefix_blocks, suffix_blocks;
+};
+Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_suffix);
 
 // Host check of int32 device data (check.hip): n entries within [lo, hi].  With
 // `len`, the entries are runs of `row`, of which run i uses the first

@@ -271,11 +271,11 @@ enum { LFM2SC_CACHE_E4M3 = 0, LFM2SC_CACHE_INT8 = 1 };
  * A block's scale, from the magnitudes of the rows alone that join it (infinities and
  * NaN apart): where the block holds no earlier token, for INT8 the largest magnitude /
  * 127 and for E4M3 the lowest power of two s with magnitudes <= 448 s (both at least
- * 2^-120; 0 if all are 0); where it does (tokens before seq_len - n), the old scale
+ * 2^-100; 0 if all are 0); where it does (tokens before seq_len - n), the old scale
  * times the lowest power of two >= 1 that holds the rows (codes up to 127.5 before
  * rounding, or 448), and the earlier codes are rounded again in steps of the new one,
  * so that a value stays within one step, however many rows follow.  (An old scale of
- * 0 or below 2^-120, or 2^40 times too small, makes a new one and zeros of the earlier codes.)
+ * 0 or below 2^-100, or 2^40 times too small, makes a new one and zeros of the earlier codes.)
  * A code is x * (1 / s) rounded to nearest even; beyond the largest it is the largest
  * (infinities too), a NaN is NaN (E4M3) or 0 (INT8).
  * In the blocks that the call touches, codes of tokens from seq_len on are not values

@@ -10,7 +10,7 @@ import numpy as np
 from oracle.hybrid import _probabilities, f64
 
 F32 = np.float32
-MIN_SCALE = F32(2.0 ** -120)
+MIN_SCALE = F32(2.0 ** -100)
 
 
 # ---------------------------------------------------------------- rotary

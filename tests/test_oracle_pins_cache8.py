@@ -23,8 +23,8 @@ def test_codes_are_torchs_float8():
 
 
 @pytest.mark.parametrize("top,int8,scale", [
-    (254.0, True, 2.0), (0.0, True, 0.0), (1e-38, True, 2.0 ** -120), (448.0, False, 1.0), (449.0, False, 2.0), (224.0, False, 0.5),
-    (225.0, False, 1.0), (1.0, False, 2.0 ** -8), (0.0, False, 0.0), (1e-38, False, 2.0 ** -120), (3e38, False, 2.0 ** 120)])
+    (254.0, True, 2.0), (0.0, True, 0.0), (1e-38, True, 2.0 ** -100), (448.0, False, 1.0), (449.0, False, 2.0), (224.0, False, 0.5),
+    (225.0, False, 1.0), (1.0, False, 2.0 ** -8), (0.0, False, 0.0), (1e-38, False, 2.0 ** -100), (3e38, False, 2.0 ** 120)])
 def test_fresh_scales(top, int8, scale):
     got = o8.fresh(np.float32(top), int8)
     assert got.dtype == np.float32 and got == np.float32(scale)
@@ -39,7 +39,7 @@ def test_joined_scales():
     assert o8.joined(np.float32(0.5), 225.0, False) == (1.0, 0.5)
     assert o8.joined(np.float32(0.0), 127.0, True) == (1.0, 0.0)
     assert o8.joined(np.float32(np.nan), 127.0, True) == (1.0, 0.0)
-    assert o8.joined(np.float32(2.0 ** -100), 127.0, True) == (1.0, 0.0)  # 2^100 times too small
+    assert o8.joined(np.float32(2.0 ** -90), 127.0, True) == (1.0, 0.0)  # 2^90 times too small
 
 
 def _cache(int8, P, H, S, D, B):
