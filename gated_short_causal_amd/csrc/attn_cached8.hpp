@@ -98,7 +98,16 @@ template <int D, bool kInt8, bool kToken>
 struct Loader8 {
     const Cached8Args& a;
     const Keys8& s;
-    int kvh, lane;
+    int lane, S;
+    const uint8_t *k, *v;    // the lane's place in a page, without its 16 tokens'
+    int scale_at;
+    __device__ __forceinline__ Loader8(const Cached8Args& a_, const Keys8& s_, int kvh, int lane_) : a(a_), s(s_), lane(lane_) {
+        const int c = lane & 15, g = lane >> 4;
+        S = 1 << a.c.page_shift;
+        k = a.k + kvh * S * D + (c & 3) * D + D / 4 * g;
+        v = a.v + kvh * S * D + c * 16;
+        scale_at = kvh * S + (kToken ? c : 0);
+    }
     // a tile's first key, its part, and the keys of the part
     __device__ __forceinline__ bool is_prefix(int i) const { return i < s.ptiles; }
     __device__ __forceinline__ int first_key(int i) const {
@@ -112,43 +121,34 @@ struct Loader8 {
     __device__ __forceinline__ int32_t page(int i, int x) const {
         return (is_prefix(i) ? s.prefix : s.own)[group_key(i, x) >> a.c.page_shift];
     }
-    __device__ __forceinline__ int clamp_page(int32_t p) const { return min(max(p, 0), a.c.num_pages - 1); }
-    // block 0's codes of the lane, and channel c's
+    // groups of the lane's keys and of its values
+    __device__ __forceinline__ int key_group() const { return (lane & 15) >> 2; }
+    __device__ __forceinline__ int value_group() const { return lane >> 4; }
+    __device__ __forceinline__ uint32_t in_pool(int32_t p) const { return (uint32_t)min(max(p, 0), a.c.num_pages - 1); }
+    // block 0's codes of the lane; channel c's 16 codes
     __device__ __forceinline__ const uint8_t* key_at(int i, int32_t pk) const {
-        const int c = lane & 15, g = lane >> 4, S = 1 << a.c.page_shift;
-        const int in = group_key(i, c >> 2) & (S - 1);
-        return a.k + (int64_t)clamp_page(pk) * a.page_stride + ((int64_t)kvh * S + in + (c & 3)) * D + D / 4 * g;
+        return k + in_pool(pk) * (uint64_t)(uint32_t)a.page_stride + (group_key(i, key_group()) & (S - 1)) * D;
     }
     __device__ __forceinline__ const uint8_t* value_at(int i, int32_t pg) const {
-        const int c = lane & 15, g = lane >> 4, S = 1 << a.c.page_shift;
-        const int in = group_key(i, g) & (S - 1);
-        return a.v + (int64_t)clamp_page(pg) * a.page_stride + ((int64_t)kvh * S + in) * D + c * 16;
+        return v + in_pool(pg) * (uint64_t)(uint32_t)a.page_stride + (group_key(i, value_group()) & (S - 1)) * D;
     }
-    // 16 codes: part h of block b, and 16 tokens of channel 16 b + c
-    __device__ __forceinline__ uint4 load_key(int i, int b, int h, int32_t pk) const {
-        return *reinterpret_cast<const uint4*>(key_at(i, pk) + 4 * b * D + 16 * h);
-    }
-    __device__ __forceinline__ uint4 load_value(int i, int b, int32_t pg) const {
-        return *reinterpret_cast<const uint4*>(value_at(i, pg) + 256 * b);
-    }
-    __device__ __forceinline__ void load_k(Tile8<D>& t, int i, int32_t pk, int32_t pg) const {
+    __device__ __forceinline__ void load_k(Tile8<D>& t, int i, int32_t pk) const {
         const uint8_t* p = key_at(i, pk);
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) t.k[b][h] = *reinterpret_cast<const uint4*>(p + 4 * b * D + 16 * h);
-        t.ks = scale(a.k_scales, i, pg);
     }
     __device__ __forceinline__ void load_v(Tile8<D>& t, int i, int32_t pg) const {
         const uint8_t* p = value_at(i, pg);
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) t.v[b] = *reinterpret_cast<const uint4*>(p + b * 256);
-        t.vs = scale(a.v_scales, i, pg);
     }
-    __device__ __forceinline__ float scale(const float* scales, int i, int32_t pg) const {
-        const int c = lane & 15, g = lane >> 4, S = 1 << a.c.page_shift;
-        const int in = (group_key(i, g) & (S - 1)) + (kToken ? c : 0);
-        return scales[(int64_t)clamp_page(pg) * a.scale_stride + (((int64_t)kvh * S + in) >> a.block_shift)];
+    __device__ __forceinline__ void load_scales(float& ks, float& vs, int i, int32_t pg) const {
+        const int64_t at = (int64_t)(in_pool(pg) * (uint64_t)(uint32_t)a.scale_stride) +
+                           ((scale_at + (group_key(i, value_group()) & (S - 1))) >> a.block_shift);
+        ks = a.k_scales[at];
+        vs = a.v_scales[at];
     }
 };
 
@@ -183,6 +183,10 @@ struct Rows8 {
 // counts as 2^-100, so that its logarithm and reciprocal exist; a NaN stays.
 __device__ __forceinline__ float usable(float scale) { return scale < kMinScale ? kMinScale : scale; }
 
+// Few tiles are masked: what only they need is a branch of its own, not selects in
+// every tile (30 instructions of each row tile's 150).
+__device__ __forceinline__ void masked_side() { asm volatile("; masked" ::: "memory"); }
+
 // Keys that do not exist, from `end` on within the tile: no scale, and (e4m3, where
 // they are in registers) zeros for their values' codes: a NaN among them would
 // outlive its probability of 0.
@@ -212,7 +216,7 @@ struct Scales8 {
         if constexpr (!kToken) {
             v = usable(vs);
             log_v = __builtin_amdgcn_logf(v);
-            const float r = 1.f / v, hi = __uint_as_float(__float_as_uint(r) & 0xffff0000u);
+            const float r = __builtin_amdgcn_rcpf(v), hi = __uint_as_float(__float_as_uint(r) & 0xffff0000u);
             const int c = lane & 15;
             const uint32_t one1 = c < 2 ? Elem<uint16_t>::pack2(c ? r - hi : hi, c ? r - hi : hi) : 0u;
             one = __builtin_bit_cast(bf16x8, make_uint4(one1, one1, one1, one1));
@@ -220,60 +224,87 @@ struct Scales8 {
     }
 };
 
-// The scores of a tile, s[t][i] of key 16 g + 4 t + i, become probabilities times
-// their values' scales: the operands p of the second product.  masked (uniform):
-// keys numbered above `seen` within the tile are masked.
+// The scores of a tile, s[t][i] of key 16 g + 4 t + i, first move the rows'
+// reference where they pass it by 2^kLazy.  masked: keys numbered above seen[n]
+// within the tile are -inf from here on (masked: uniform).
 template <int D, int NT, bool kToken>
-__device__ __forceinline__ void softmax8(Rows8<D, NT, kToken>& r, int n, const f32x4 (&s)[4], bf16x8 (&p)[2], const Scales8<kToken>& sc,
-                                         bool masked, int seen, int g) {
-    float x[16];
-    for_keys([&](auto i) {
-        constexpr int e = decltype(i)::value;
-        if constexpr (kToken) x[e] = s[e >> 2][e & 3] * row_lane<e>(sc.k);
-        else x[e] = s[e >> 2][e & 3];
-    });
-    if (masked) {
+__device__ __forceinline__ void refer8(Rows8<D, NT, kToken>& r, f32x4 (&s)[NT][4], const Scales8<kToken>& sc, bool masked,
+                                       const int (&seen)[NT], int g) {
+    float mn[NT];
+    bool move = false;
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-            if (16 * g + e > seen) x[e] = kNegInf;
-    }
-    float mx = x[0];
+    for (int n = 0; n < NT; ++n) {
+        if constexpr (kToken)
+            for_keys([&](auto i) {
+                constexpr int e = decltype(i)::value;
+                s[n][e >> 2][e & 3] *= row_lane<e>(sc.k);
+            });
+        if (masked) {
+            masked_side();
 #pragma unroll
-    for (int e = 1; e < 16; ++e) mx = fmaxf(mx, x[e]);
-    const float mn = max_groups(kToken ? mx : mx * sc.k);
-    if (__any(mn > r.m[n] + kLazy)) {
-        const float m = fmaxf(r.m[n], mn), alpha = exp2_fast(r.m[n] - (m == kNegInf ? 0.f : m));
-        r.m[n] = m;
-        r.l[n] *= alpha;
-#pragma unroll
-        for (int b = 0; b < D / 16; ++b) r.o[n][b] *= alpha;
-    }
-    const float ref = r.m[n] == kNegInf ? 0.f : r.m[n];
-    if constexpr (kToken) {
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            x[e] = exp2_fast(x[e] - ref);
-            sum += x[e];
+            for (int e = 0; e < 16; ++e)
+                if (16 * g + e > seen[n]) s[n][e >> 2][e & 3] = kNegInf;
         }
-        r.l[n] += sum;
-        for_keys([&](auto i) {
-            constexpr int e = decltype(i)::value;
-            x[e] *= row_lane<e>(sc.v);
-        });
-    } else {
-        const float at = sc.log_v - ref;         // p vs = 2^(score - ref + log2 vs)
+        float mx = s[n][0][0];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) x[e] = exp2_fast(__builtin_fmaf(x[e], sc.k, at));
+        for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[n][e >> 2][e & 3]);
+        mn[n] = max_groups(kToken ? mx : mx * sc.k);
+        move |= mn[n] > r.m[n] + kLazy;
     }
+    if (__any(move)) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
+        for (int n = 0; n < NT; ++n) {
+            const float m = mn[n] > r.m[n] + kLazy ? mn[n] : r.m[n];
+            const float alpha = exp2_fast(r.m[n] - (m == kNegInf ? 0.f : m));
+            r.m[n] = m;
+            r.l[n] *= alpha;
+#pragma unroll
+            for (int b = 0; b < D / 16; ++b) r.o[n][b] *= alpha;
+        }
+    }
+}
+
+// Then the scores of block b become probabilities times their values' scales, words
+// 2 (b & 1) and + 1 of operand b >> 1 of the second product.  between() runs when
+// the scores have been read.
+template <int b, int D, int NT, bool kToken, typename F>
+__device__ __forceinline__ void weigh8(Rows8<D, NT, kToken>& r, f32x4 (&s)[NT][4], bf16x8 (&p)[NT][2], const Scales8<kToken>& sc, F between) {
+    float x[NT][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float ref = r.m[n] == kNegInf ? 0.f : r.m[n], at = kToken ? -ref : sc.log_v - ref;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)              // else: p vs = 2^(score - ref + log2 vs)
+            x[n][i] = kToken ? s[n][b][i] + at : __builtin_fmaf(s[n][b][i], sc.k, at);
+    }
+    between();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[n][i] = exp2_fast(x[n][i]);
+        if constexpr (kToken) {
+            r.l[n] += (x[n][0] + x[n][1]) + (x[n][2] + x[n][3]);
+            x[n][0] *= row_lane<4 * b>(sc.v);
+            x[n][1] *= row_lane<4 * b + 1>(sc.v);
+            x[n][2] *= row_lane<4 * b + 2>(sc.v);
+            x[n][3] *= row_lane<4 * b + 3>(sc.v);
+        }
         union { uint32_t w[4]; bf16x8 v; } y;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y.w[j] = Elem<uint16_t>::pack2(x[8 * u + 2 * j], x[8 * u + 2 * j + 1]);
-        p[u] = y.v;
-        if constexpr (!kToken) r.l[n] = mfma16(sc.one, y.v, r.l[n]);
+        y.v = p[n][b >> 1];
+        y.w[2 * (b & 1)] = Elem<uint16_t>::pack2(x[n][0], x[n][1]);
+        y.w[2 * (b & 1) + 1] = Elem<uint16_t>::pack2(x[n][2], x[n][3]);
+        p[n][b >> 1] = y.v;
     }
+}
+
+// l of a block-scaled row.
+template <int D, int NT, bool kToken>
+__device__ __forceinline__ void sum8(Rows8<D, NT, kToken>& r, const bf16x8 (&p)[NT][2], const Scales8<kToken>& sc) {
+    if constexpr (!kToken)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) r.l[n] = mfma16(sc.one, p[n][u], r.l[n]);
 }
 
 // One tile, in registers, against the wave's rows.
@@ -301,12 +332,17 @@ __device__ __forceinline__ void attend8(Rows8<D, NT, kToken>& r, const bf16x8 (&
     sc.set(t.ks, t.vs, cs, masked, end, lane);
     after_k();
     if (!kInt8 && masked) {
+        masked_side();
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) drop_codes(t.v[b], end - 16 * g);
     }
+    refer8<D, NT, kToken>(r, s, sc, masked, seen, g);
     bf16x8 p[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) softmax8<D, NT, kToken>(r, n, s[n], p[n], sc, masked, seen[n], g);
+    weigh8<0>(r, s, p, sc, [] {});
+    weigh8<1>(r, s, p, sc, [] {});
+    weigh8<2>(r, s, p, sc, [] {});
+    weigh8<3>(r, s, p, sc, [] {});
+    sum8<D, NT, kToken>(r, p, sc);
 #pragma unroll
     for (int b = 0; b < D / 16; ++b) {
         const bf16x8 v0 = codes_to_bf16<kInt8>(t.v[b].x, t.v[b].y), v1 = codes_to_bf16<kInt8>(t.v[b].z, t.v[b].w);
@@ -326,17 +362,17 @@ template <int D, int NT, bool kInt8, bool kToken>
 __device__ __forceinline__ void walk8(Rows8<D, NT, kToken>& r, const bf16x8 (&q)[NT][D / 32], const Cached8Args& a, const Keys8& s,
                                       int kvh, int tiles, int mine, int step, const int (&last)[NT], int least, int lane) {
     if (mine >= tiles) return;
-    const int c = lane & 15, g = lane >> 4;
-    const Loader8<D, kInt8, kToken> ld{a, s, kvh, lane};
+    const Loader8<D, kInt8, kToken> ld(a, s, kvh, lane);
     const float cs = a.c.scale * kLog2e;
     Tile8<D> t;
-    int32_t pk = ld.page(mine, c >> 2), pg = ld.page(mine, g);
-    ld.load_k(t, mine, pk, pg);
+    int32_t pk = ld.page(mine, ld.key_group()), pg = ld.page(mine, ld.value_group());
+    ld.load_k(t, mine, pk);
+    ld.load_scales(t.ks, t.vs, mine, pg);
     ld.load_v(t, mine, pg);
     int32_t nk = 0, ng = 0;
     if (mine + step < tiles) {
-        nk = ld.page(mine + step, c >> 2);
-        ng = ld.page(mine + step, g);
+        nk = ld.page(mine + step, ld.key_group());
+        ng = ld.page(mine + step, ld.value_group());
     }
     for (int i = mine; i < tiles; i += step) {
         const bool prefix = ld.is_prefix(i);
@@ -344,20 +380,21 @@ __device__ __forceinline__ void walk8(Rows8<D, NT, kToken>& r, const bf16x8 (&q)
         int seen[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) seen[n] = prefix ? end - 1 : last[n] - k0;
-        const bool masked = prefix ? end < kC8Tile : k0 + kC8Tile - 1 > least;
         const int next = i + step;
         auto after_k = [&] {
             if (next >= tiles) return;
             pk = nk;
             pg = ng;
             const int then = min(next + step, tiles - 1);
-            nk = ld.page(then, c >> 2);
-            ng = ld.page(then, g);
-            ld.load_k(t, next, pk, pg);
+            nk = ld.page(then, ld.key_group());
+            ng = ld.page(then, ld.value_group());
+            ld.load_k(t, next, pk);
+            ld.load_scales(t.ks, t.vs, next, pg);
         };
         auto after_v = [&] {
             if (next < tiles) ld.load_v(t, next, pg);
         };
+        const bool masked = prefix ? end < kC8Tile : k0 + kC8Tile - 1 > least;
         attend8<D, NT, kInt8, kToken>(r, q, t, cs, masked, seen, end, lane, after_k, after_v);
     }
 }
@@ -470,15 +507,17 @@ __device__ __forceinline__ void keys8(const Cached8Args& a, const Keys8& s, int 
 
 // Prefix keys for many rows: 8 waves of 32 query rows share each tile.  They turn
 // its codes into bf16 operands once, in LDS in the order in which the products
-// read them (operand, lane: 16 bytes each, no bank conflict), two buffers, one
-// barrier a tile; the next tile's codes are in registers meanwhile.
+// read them (operand, lane: 16 bytes each, no bank conflict), two buffers of K and
+// of V, one barrier a tile.  The scores run a tile ahead: between two barriers a
+// wave turns the scores of tile i into p while the matrix unit forms those of tile
+// i + 1, then adds p V.
 constexpr int kSharedRows = 32 * 8;
 template <int D>
-constexpr int shared_bytes() { return 2 * kC8Tile * D * 2; }       // a buffer: K and V of a tile
+constexpr int shared_bytes() { return 4 * kC8Tile * D * 2; }
 template <int D, bool kInt8, bool kToken>
 __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, int kvh, int x0, int rows, int split, uint4* lds, int wave,
                                         int lane) {
-    constexpr int NT = 2, kKey = 4 * (D / 32) * 64, kBuf = shared_bytes<D>() / 16;
+    constexpr int NT = 2, kBuf = kC8Tile * D * 2 / 16;
     const CachedArgs& ca = a.c;
     const int c = lane & 15, g = lane >> 4;
     x0 += 32 * wave;
@@ -489,80 +528,127 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
         const Query8 y = query8(ca, kvh, x0 + 16 * n + c, rows);
         load_query8<D>(q[n], ca.q + y.token * ca.q_stride + y.head * D, g, y.exists);
     }
-    const Loader8<D, kInt8, kToken> ld{a, s, kvh, lane};
+    const Loader8<D, kInt8, kToken> ld(a, s, kvh, lane);
     const float cs = ca.scale * kLog2e;
+    const int tiles = s.ptiles;
     Rows8<D, NT, kToken> r;
     r.clear();
     // D = 128: wave w brings half (w & 1) of the keys' block w >> 1, and channels 16 w ..; D = 64: waves 0 to 3 a block of
     // keys each, waves 4 to 7 16 channels each.
+    const bool brings_k = D == 128 || wave < 4, brings_v = D == 128 || wave >= 4;
+    const int kb = D == 128 ? wave >> 1 : wave, kh = D == 128 ? wave & 1 : 0, vb = D == 128 ? wave : wave & 3;
     uint4 kc, vc;
     float ks, vs;
-    auto load = [&](int i, int32_t pk, int32_t pg) {
-        if (D == 128 || wave < 4) kc = ld.load_key(i, D == 128 ? wave >> 1 : wave, D == 128 ? wave & 1 : 0, pk);
-        if (D == 128 || wave >= 4) vc = ld.load_value(i, D == 128 ? wave : wave - 4, pg);
-        ks = ld.scale(a.k_scales, i, pg);
-        vs = ld.scale(a.v_scales, i, pg);
+    auto load_k = [&](int i, int32_t pk) {
+        if (brings_k) kc = *reinterpret_cast<const uint4*>(ld.key_at(i, pk) + 4 * kb * D + 16 * kh);
     };
-    auto stage = [&](uint4* buf, int i) {
-        const int end = ld.end_key(i) - ld.first_key(i);
-        if (D == 128 || wave < 4) {
-            uint4* p = buf + (D == 128 ? (wave >> 1) * 4 + (wave & 1) * 2 : wave * 2) * 64 + lane;
-            p[0] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(kc.x, kc.y));
-            p[64] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(kc.z, kc.w));
-        }
-        if (D == 128 || wave >= 4) {
-            if (!kInt8 && end < kC8Tile) drop_codes(vc, end - 16 * g);
-            uint4* p = buf + kKey + (D == 128 ? wave : wave - 4) * 2 * 64 + lane;
-            p[0] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(vc.x, vc.y));
-            p[64] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(vc.z, vc.w));
-        }
+    auto load_v = [&](int i, int32_t pg) {
+        if (brings_v) vc = *reinterpret_cast<const uint4*>(ld.value_at(i, pg) + 256 * vb);
+        ld.load_scales(ks, vs, i, pg);
     };
-    load(0, ld.page(0, c >> 2), ld.page(0, g));
-    int32_t nk = 0, ng = 0;
-    if (s.ptiles > 1) {
-        nk = ld.page(1, c >> 2);
-        ng = ld.page(1, g);
-    }
-    for (int i = 0; i < s.ptiles; ++i) {
-        uint4* buf = lds + (i & 1) * kBuf;
-        stage(buf, i);
-        const int end = ld.end_key(i) - ld.first_key(i);
-        const bool masked = end < kC8Tile;
-        Scales8<kToken> f;
-        f.set(ks, vs, cs, masked, end, lane);
-        if (i + 1 < s.ptiles) {
-            const int32_t pk = nk, pg = ng;
-            const int then = min(i + 2, s.ptiles - 1);
-            nk = ld.page(then, c >> 2);
-            ng = ld.page(then, g);
-            load(i + 1, pk, pg);
-        }
-        lds_barrier();
-        if (!busy) continue;
-        f32x4 sc[NT][4];
+    auto stage_k = [&](int i) {
+        if (!brings_k) return;
+        uint4* p = lds + (i & 1) * kBuf + (kb * (D / 32) + 2 * kh) * 64 + lane;
+        p[0] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(kc.x, kc.y));
+        p[64] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(kc.z, kc.w));
+    };
+    auto stage_v = [&](int i, int end) {
+        if (!brings_v) return;
+        if (!kInt8 && end < kC8Tile) drop_codes(vc, end - 16 * g);
+        uint4* p = lds + (2 + (i & 1)) * kBuf + vb * 2 * 64 + lane;
+        p[0] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(vc.x, vc.y));
+        p[64] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(vc.z, vc.w));
+    };
+    auto read_k = [&](bf16x8 (&k)[D / 32], int i, int b) {
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) k[d] = __builtin_bit_cast(bf16x8, lds[(i & 1) * kBuf + (b * (D / 32) + d) * 64 + lane]);
+    };
+    auto read_v = [&](bf16x8 (&v)[2], int i, int b) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) v[u] = __builtin_bit_cast(bf16x8, lds[(2 + (i & 1)) * kBuf + (b * 2 + u) * 64 + lane]);
+    };
+    auto products = [&](f32x4 (&sc)[NT][4], const bf16x8 (&k)[D / 32], int b) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) sc[n][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sc[n][b] = mfma16(k[d], q[n][d], sc[n][b]);
+    };
+    // Before a step: tile i's scores, its V codes and scales and the K codes of tile i + 1 are in registers.
+    int32_t pk = ld.page(0, ld.key_group()), pg = ld.page(0, ld.value_group());
+    int32_t nk = ld.page(min(1, tiles - 1), ld.key_group()), ng = ld.page(min(1, tiles - 1), ld.value_group());
+    load_k(0, pk);
+    stage_k(0);
+    load_v(0, pg);
+    load_k(min(1, tiles - 1), nk);
+    lds_barrier();
+    f32x4 sc[NT][4];
+    if (busy) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) sc[n][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int d = 0; d < D / 32; ++d) {
-                const bf16x8 k = __builtin_bit_cast(bf16x8, buf[(b * (D / 32) + d) * 64 + lane]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) sc[n][b] = mfma16(k, q[n][d], sc[n][b]);
-            }
+            bf16x8 k[D / 32];
+            read_k(k, 0, b);
+            products(sc, k, b);
         }
-        bf16x8 p[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) softmax8<D, NT, kToken>(r, n, sc[n], p[n], f, masked, end - 1, g);
-#pragma unroll
-        for (int b = 0; b < D / 16; ++b)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const bf16x8 v = __builtin_bit_cast(bf16x8, buf[kKey + (b * 2 + u) * 64 + lane]);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) r.o[n][b] = mfma16(v, p[n][u], r.o[n][b]);
-            }
     }
+    auto step = [&](auto last_c, int i) {
+        constexpr bool last = decltype(last_c)::value;       // the part may end within its last tile
+        const int end = ld.end_key(i) - ld.first_key(i);
+        stage_v(i, last ? end : kC8Tile);
+        Scales8<kToken> f;
+        f.set(ks, vs, cs, last && end < kC8Tile, end, lane);
+        if constexpr (!last) {
+            stage_k(i + 1);
+            const int then = min(i + 2, tiles - 1);
+            pg = ng;
+            nk = ld.page(then, ld.key_group());
+            ng = ld.page(then, ld.value_group());
+            load_v(i + 1, pg);
+            load_k(then, nk);
+        }
+        lds_barrier();
+        if (!busy) return;
+        const int seen[NT] = {end - 1, end - 1};
+        refer8<D, NT, kToken>(r, sc, f, last && end < kC8Tile, seen, g);
+        // Operands are read one block ahead of their products; the regions keep the compiler from reading them all first.
+        bf16x8 p[NT][2], k[D / 32], v[2];
+        if constexpr (!last) read_k(k, i + 1, 0);
+        auto quarter = [&](auto b_c) {
+            constexpr int b = decltype(b_c)::value;
+            bf16x8 next[D / 32];
+            if constexpr (!last && b < 3) read_k(next, i + 1, b + 1);
+            if constexpr (b == 3) read_v(v, i, 0);
+            weigh8<b>(r, sc, p, f, [&] {
+                if constexpr (!last) products(sc, k, b);
+            });
+            if constexpr (!last && b < 3)
+#pragma unroll
+                for (int d = 0; d < D / 32; ++d) k[d] = next[d];
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        quarter(IC<0>{});
+        quarter(IC<1>{});
+        quarter(IC<2>{});
+        quarter(IC<3>{});
+        sum8<D, NT, kToken>(r, p, f);
+#pragma unroll
+        for (int b = 0; b < D / 16; ++b) {
+            bf16x8 next[2];
+            if (b + 1 < D / 16) read_v(next, i, b + 1);
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int n = 0; n < NT; ++n) r.o[n][b] = mfma16(v[u], p[n][u], r.o[n][b]);
+            if (b + 1 < D / 16) {
+                v[0] = next[0];
+                v[1] = next[1];
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    for (int i = 0; i + 1 < tiles; ++i) step(std::false_type{}, i);
+    step(std::true_type{}, tiles - 1);
     float l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) l[n] = r.sum(n);
@@ -577,7 +663,7 @@ enum Form8 { kDirect8, kSplit8, kShared8 };
 constexpr int form_waves(int form) { return form == kSplit8 ? 4 : 8; }
 // waves a SIMD, which bounds their registers: 128, 168 or 256 of 512
 constexpr int form_per_simd(int D, int NT, int form) {
-    if (D == 64 && NT == 1) return 4;
+    if (D == 64 && NT == 1) return form == kShared8 ? 2 : 4;
     return form == kSplit8 && (D == 64 || NT == 1) ? 3 : 2;
 }
 constexpr int own_waves(int form) { return form == kDirect8 ? 8 : 4; }
@@ -586,7 +672,7 @@ template <int D, int NT, bool kInt8, bool kToken, int kForm>
 __global__ __launch_bounds__(64 * form_waves(kForm), form_per_simd(D, NT, kForm)) void attn_cached8_kernel(Cached8Args a) {
     constexpr int W = form_waves(kForm), U = own_waves(kForm);
     constexpr int kJoin = W / 2 * join_floats<D, NT>() * 4;
-    constexpr int kLds = kForm == kShared8 && 2 * shared_bytes<D>() > kJoin ? 2 * shared_bytes<D>() : kJoin;
+    constexpr int kLds = kForm == kShared8 && shared_bytes<D>() > kJoin ? shared_bytes<D>() : kJoin;
     __shared__ uint4 lds[kLds / 16];
     const CachedArgs& ca = a.c;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
