@@ -94,19 +94,31 @@ struct Keys8 {
     int tile0;               // first own tile
 };
 
-template <int D, bool kInt8, bool kToken>
+// Addresses of a tile.  A tile begins at a multiple of 64 keys, so its offset in a
+// page is uniform (0 in pages of up to 64 tokens), and a lane's 16 tokens lie at the
+// same distance from it in every tile: an address is a constant of the lane, one
+// product with a page number and the uniform offset.  No branch on the page size:
+// the loads in flight are then counted exactly.  Tokens past the end are read from
+// the last page that exists.
+struct Pages8 {
+    int32_t k, v;            // page numbers: of the lane's keys, of its values
+};
+template <int D, bool kToken>
 struct Loader8 {
     const Cached8Args& a;
     const Keys8& s;
-    int lane, S;
-    const uint8_t *k, *v;    // the lane's place in a page, without its 16 tokens'
-    int scale_at;
+    int lane, shift;
+    const uint8_t *k, *v;    // the lane's place in page 0
+    const float *ks, *vs;
     __device__ __forceinline__ Loader8(const Cached8Args& a_, const Keys8& s_, int kvh, int lane_) : a(a_), s(s_), lane(lane_) {
         const int c = lane & 15, g = lane >> 4;
-        S = 1 << a.c.page_shift;
-        k = a.k + kvh * S * D + (c & 3) * D + D / 4 * g;
-        v = a.v + kvh * S * D + c * 16;
-        scale_at = kvh * S + (kToken ? c : 0);
+        shift = a.c.page_shift;
+        const int S = 1 << shift, kin = (16 * key_group()) & (S - 1), vin = (16 * g) & (S - 1);
+        k = a.k + (kvh * S + kin + (c & 3)) * D + D / 4 * g;
+        v = a.v + (kvh * S + vin) * D + c * 16;
+        const int at = (kvh * S + vin + (kToken ? c : 0)) >> a.block_shift;
+        ks = a.k_scales + at;
+        vs = a.v_scales + at;
     }
     // a tile's first key, its part, and the keys of the part
     __device__ __forceinline__ bool is_prefix(int i) const { return i < s.ptiles; }
@@ -114,41 +126,40 @@ struct Loader8 {
         return i < s.ptiles ? s.p0 + i * kC8Tile : (s.tile0 + i - s.ptiles) * kC8Tile;
     }
     __device__ __forceinline__ int end_key(int i) const { return i < s.ptiles ? s.p1 : s.len; }
-    // 16 tokens of a page: those of group x of tile i, or the last ones that exist
-    __device__ __forceinline__ int group_key(int i, int x) const {
-        return min(first_key(i) + 16 * x, (end_key(i) - 1) & ~15);
-    }
-    __device__ __forceinline__ int32_t page(int i, int x) const {
-        return (is_prefix(i) ? s.prefix : s.own)[group_key(i, x) >> a.c.page_shift];
-    }
-    // groups of the lane's keys and of its values
+    // groups of 16 tokens of the tile: of the lane's keys, of its values
     __device__ __forceinline__ int key_group() const { return (lane & 15) >> 2; }
     __device__ __forceinline__ int value_group() const { return lane >> 4; }
-    __device__ __forceinline__ uint32_t in_pool(int32_t p) const { return (uint32_t)min(max(p, 0), a.c.num_pages - 1); }
-    // block 0's codes of the lane; channel c's 16 codes
-    __device__ __forceinline__ const uint8_t* key_at(int i, int32_t pk) const {
-        return k + in_pool(pk) * (uint64_t)(uint32_t)a.page_stride + (group_key(i, key_group()) & (S - 1)) * D;
+    __device__ __forceinline__ Pages8 pages(int i) const {
+        const int32_t* table = is_prefix(i) ? s.prefix : s.own;
+        const int first = first_key(i), last = (end_key(i) - 1) >> shift;
+        return Pages8{table[(uint32_t)min((first + 16 * key_group()) >> shift, last)],
+                      table[(uint32_t)min((first + 16 * value_group()) >> shift, last)]};
     }
-    __device__ __forceinline__ const uint8_t* value_at(int i, int32_t pg) const {
-        return v + in_pool(pg) * (uint64_t)(uint32_t)a.page_stride + (group_key(i, value_group()) & (S - 1)) * D;
+    __device__ __forceinline__ uint32_t in_page(int i) const { return (uint32_t)(first_key(i) & ((1 << shift) - 1)); }
+    __device__ __forceinline__ uint64_t in_pool(int32_t p) const { return (uint32_t)min(max(p, 0), a.c.num_pages - 1); }
+    __device__ __forceinline__ const uint8_t* key_at(int i, const Pages8& p) const {
+        return k + in_pool(p.k) * (uint32_t)a.page_stride + in_page(i) * D;
     }
-    __device__ __forceinline__ void load_k(Tile8<D>& t, int i, int32_t pk) const {
-        const uint8_t* p = key_at(i, pk);
+    __device__ __forceinline__ const uint8_t* value_at(int i, const Pages8& p) const {
+        return v + in_pool(p.v) * (uint32_t)a.page_stride + in_page(i) * D;
+    }
+    __device__ __forceinline__ void load_k(Tile8<D>& t, int i, const Pages8& g) const {
+        const uint8_t* p = key_at(i, g);
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) t.k[b][h] = *reinterpret_cast<const uint4*>(p + 4 * b * D + 16 * h);
     }
-    __device__ __forceinline__ void load_v(Tile8<D>& t, int i, int32_t pg) const {
-        const uint8_t* p = value_at(i, pg);
+    __device__ __forceinline__ void load_v(Tile8<D>& t, int i, const Pages8& g) const {
+        const uint8_t* p = value_at(i, g);
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) t.v[b] = *reinterpret_cast<const uint4*>(p + b * 256);
     }
-    __device__ __forceinline__ void load_scales(float& ks, float& vs, int i, int32_t pg) const {
-        const int64_t at = (int64_t)(in_pool(pg) * (uint64_t)(uint32_t)a.scale_stride) +
-                           ((scale_at + (group_key(i, value_group()) & (S - 1))) >> a.block_shift);
-        ks = a.k_scales[at];
-        vs = a.v_scales[at];
+    __device__ __forceinline__ void load_scales(float& k1, float& v1, int i, const Pages8& g) const {
+        // The offset, a multiple of 64, and the lane's tokens below 64 do not carry into each other's part of the block number.
+        const uint64_t at = in_pool(g.v) * (uint32_t)a.scale_stride + (in_page(i) >> a.block_shift);
+        k1 = ks[at];
+        v1 = vs[at];
     }
 };
 
@@ -362,18 +373,14 @@ template <int D, int NT, bool kInt8, bool kToken>
 __device__ __forceinline__ void walk8(Rows8<D, NT, kToken>& r, const bf16x8 (&q)[NT][D / 32], const Cached8Args& a, const Keys8& s,
                                       int kvh, int tiles, int mine, int step, const int (&last)[NT], int least, int lane) {
     if (mine >= tiles) return;
-    const Loader8<D, kInt8, kToken> ld(a, s, kvh, lane);
+    const Loader8<D, kToken> ld(a, s, kvh, lane);
     const float cs = a.c.scale * kLog2e;
     Tile8<D> t;
-    int32_t pk = ld.page(mine, ld.key_group()), pg = ld.page(mine, ld.value_group());
-    ld.load_k(t, mine, pk);
-    ld.load_scales(t.ks, t.vs, mine, pg);
-    ld.load_v(t, mine, pg);
-    int32_t nk = 0, ng = 0;
-    if (mine + step < tiles) {
-        nk = ld.page(mine + step, ld.key_group());
-        ng = ld.page(mine + step, ld.value_group());
-    }
+    Pages8 now = ld.pages(mine), ahead{0, 0};
+    ld.load_k(t, mine, now);
+    ld.load_scales(t.ks, t.vs, mine, now);
+    ld.load_v(t, mine, now);
+    if (mine + step < tiles) ahead = ld.pages(mine + step);
     for (int i = mine; i < tiles; i += step) {
         const bool prefix = ld.is_prefix(i);
         const int k0 = ld.first_key(i), end = ld.end_key(i) - k0;
@@ -383,16 +390,13 @@ __device__ __forceinline__ void walk8(Rows8<D, NT, kToken>& r, const bf16x8 (&q)
         const int next = i + step;
         auto after_k = [&] {
             if (next >= tiles) return;
-            pk = nk;
-            pg = ng;
-            const int then = min(next + step, tiles - 1);
-            nk = ld.page(then, ld.key_group());
-            ng = ld.page(then, ld.value_group());
-            ld.load_k(t, next, pk);
-            ld.load_scales(t.ks, t.vs, next, pg);
+            now = ahead;
+            ahead = ld.pages(min(next + step, tiles - 1));
+            ld.load_k(t, next, now);
+            ld.load_scales(t.ks, t.vs, next, now);
         };
         auto after_v = [&] {
-            if (next < tiles) ld.load_v(t, next, pg);
+            if (next < tiles) ld.load_v(t, next, now);
         };
         const bool masked = prefix ? end < kC8Tile : k0 + kC8Tile - 1 > least;
         attend8<D, NT, kInt8, kToken>(r, q, t, cs, masked, seen, end, lane, after_k, after_v);
@@ -508,9 +512,10 @@ __device__ __forceinline__ void keys8(const Cached8Args& a, const Keys8& s, int 
 // Prefix keys for many rows: 8 waves of 32 query rows share each tile.  They turn
 // its codes into bf16 operands once, in LDS in the order in which the products
 // read them (operand, lane: 16 bytes each, no bank conflict), two buffers of K and
-// of V, one barrier a tile.  The scores run a tile ahead: between two barriers a
-// wave turns the scores of tile i into p while the matrix unit forms those of tile
-// i + 1, then adds p V.
+// of V, one barrier a tile.  With two waves a SIMD the vector unit has to work
+// beside the matrix unit within a wave: between two barriers the scores of tile i
+// turn into p while those of tile i + 1 are formed, and the codes of K in tile
+// i + 2 and of V in tile i + 1 are staged while p V is added up.
 constexpr int kSharedRows = 32 * 8;
 template <int D>
 constexpr int shared_bytes() { return 4 * kC8Tile * D * 2; }
@@ -528,36 +533,41 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
         const Query8 y = query8(ca, kvh, x0 + 16 * n + c, rows);
         load_query8<D>(q[n], ca.q + y.token * ca.q_stride + y.head * D, g, y.exists);
     }
-    const Loader8<D, kInt8, kToken> ld(a, s, kvh, lane);
+    const Loader8<D, kToken> ld(a, s, kvh, lane);
     const float cs = ca.scale * kLog2e;
     const int tiles = s.ptiles;
     Rows8<D, NT, kToken> r;
     r.clear();
-    // D = 128: wave w brings half (w & 1) of the keys' block w >> 1, and channels 16 w ..; D = 64: waves 0 to 3 a block of
-    // keys each, waves 4 to 7 16 channels each.
-    const bool brings_k = D == 128 || wave < 4, brings_v = D == 128 || wave >= 4;
-    const int kb = D == 128 ? wave >> 1 : wave, kh = D == 128 ? wave & 1 : 0, vb = D == 128 ? wave : wave & 3;
-    uint4 kc, vc;
+    // Wave w brings, of block w >> 1 of the keys, half w & 1 of a lane's codes (D = 128: 16 of them, D = 64: 8), and of V
+    // channels 16 w .. (D = 128), or 8 of a lane's 16 tokens of channels 16 (w >> 1) .. (D = 64).
+    constexpr int F = D / 64;                            // operands of a wave, of K and of V
+    using Codes = std::conditional_t<D == 128, uint4, uint2>;
+    const int kb = wave >> 1, kh = wave & 1, vb = D == 128 ? wave : wave >> 1, vh = D == 128 ? 0 : wave & 1;
+    Codes kc, vc;                                        // codes of K and V on their way to LDS
     float ks, vs;
-    auto load_k = [&](int i, int32_t pk) {
-        if (brings_k) kc = *reinterpret_cast<const uint4*>(ld.key_at(i, pk) + 4 * kb * D + 16 * kh);
+    auto tile = [&](int i) { return min(i, tiles - 1); };
+    auto load_k = [&](int i, const Pages8& p) {
+        kc = *reinterpret_cast<const Codes*>(ld.key_at(i, p) + 4 * kb * D + (D / 8) * kh);
     };
-    auto load_v = [&](int i, int32_t pg) {
-        if (brings_v) vc = *reinterpret_cast<const uint4*>(ld.value_at(i, pg) + 256 * vb);
-        ld.load_scales(ks, vs, i, pg);
+    auto load_v = [&](int i, const Pages8& p) { vc = *reinterpret_cast<const Codes*>(ld.value_at(i, p) + 256 * vb + 8 * vh); };
+    auto operand = [&](const Codes& x, int u) {
+        if constexpr (D == 128) return __builtin_bit_cast(uint4, u ? codes_to_bf16<kInt8>(x.z, x.w) : codes_to_bf16<kInt8>(x.x, x.y));
+        else return __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(x.x, x.y));
     };
-    auto stage_k = [&](int i) {
-        if (!brings_k) return;
-        uint4* p = lds + (i & 1) * kBuf + (kb * (D / 32) + 2 * kh) * 64 + lane;
-        p[0] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(kc.x, kc.y));
-        p[64] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(kc.z, kc.w));
-    };
-    auto stage_v = [&](int i, int end) {
-        if (!brings_v) return;
-        if (!kInt8 && end < kC8Tile) drop_codes(vc, end - 16 * g);
-        uint4* p = lds + (2 + (i & 1)) * kBuf + vb * 2 * 64 + lane;
-        p[0] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(vc.x, vc.y));
-        p[64] = __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(vc.z, vc.w));
+    auto stage_k = [&](int i, int u) { lds[(i & 1) * kBuf + (kb * (D / 32) + F * kh + u) * 64 + lane] = operand(kc, u); };
+    auto stage_v = [&](int i, int u) { lds[(2 + (i & 1)) * kBuf + (vb * 2 + vh + u) * 64 + lane] = operand(vc, u); };
+    auto clean_v = [&](int i) {                          // e4m3: no NaN from tokens that do not exist
+        const int end = ld.end_key(i) - ld.first_key(i);
+        if (!kInt8 && end < kC8Tile) {
+            masked_side();
+            if constexpr (D == 128) {
+                drop_codes(vc, end - 16 * g);
+            } else {
+                uint4 x = make_uint4(vc.x, vc.y, 0, 0);
+                drop_codes(x, end - 16 * g - 8 * vh);
+                vc = make_uint2(x.x, x.y);
+            }
+        }
     };
     auto read_k = [&](bf16x8 (&k)[D / 32], int i, int b) {
 #pragma unroll
@@ -575,13 +585,26 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
 #pragma unroll
             for (int n = 0; n < NT; ++n) sc[n][b] = mfma16(k[d], q[n][d], sc[n][b]);
     };
-    // Before a step: tile i's scores, its V codes and scales and the K codes of tile i + 1 are in registers.
-    int32_t pk = ld.page(0, ld.key_group()), pg = ld.page(0, ld.value_group());
-    int32_t nk = ld.page(min(1, tiles - 1), ld.key_group()), ng = ld.page(min(1, tiles - 1), ld.value_group());
-    load_k(0, pk);
-    stage_k(0);
-    load_v(0, pg);
-    load_k(min(1, tiles - 1), nk);
+    // Before step i: the scores and scales of tile i, the codes of K in tile i + 2 and of V in tile i + 1, and the page
+    // numbers of tiles i + 1 to i + 3 are in registers; K of tile i + 1 and V of tile i are staged.  Tiles past the last
+    // are the last once more.
+    Pages8 p1 = ld.pages(0), p2 = ld.pages(tile(1)), p3 = ld.pages(tile(2));
+    load_k(0, p1);
+    load_v(0, p1);
+    ld.load_scales(ks, vs, 0, p1);
+#pragma unroll
+    for (int u = 0; u < F; ++u) stage_k(0, u);
+    load_k(tile(1), p2);
+    clean_v(0);
+#pragma unroll
+    for (int u = 0; u < F; ++u) stage_v(0, u);
+    load_v(tile(1), p2);
+#pragma unroll
+    for (int u = 0; u < F; ++u) stage_k(1, u);
+    load_k(tile(2), p3);
+    p1 = p2;
+    p2 = p3;
+    p3 = ld.pages(tile(3));
     lds_barrier();
     f32x4 sc[NT][4];
     if (busy) {
@@ -592,28 +615,46 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
             products(sc, k, b);
         }
     }
+    lds_barrier();                                       // K of tile 0 is read: its buffer takes tile 2
     auto step = [&](auto last_c, int i) {
         constexpr bool last = decltype(last_c)::value;       // the part may end within its last tile
-        const int end = ld.end_key(i) - ld.first_key(i);
-        stage_v(i, last ? end : kC8Tile);
-        Scales8<kToken> f;
-        f.set(ks, vs, cs, last && end < kC8Tile, end, lane);
-        if constexpr (!last) {
-            stage_k(i + 1);
-            const int then = min(i + 2, tiles - 1);
-            pg = ng;
-            nk = ld.page(then, ld.key_group());
-            ng = ld.page(then, ld.value_group());
-            load_v(i + 1, pg);
-            load_k(then, nk);
-        }
-        lds_barrier();
-        if (!busy) return;
-        const int seen[NT] = {end - 1, end - 1};
-        refer8<D, NT, kToken>(r, sc, f, last && end < kC8Tile, seen, g);
-        // Operands are read one block ahead of their products; the regions keep the compiler from reading them all first.
         bf16x8 p[NT][2], k[D / 32], v[2];
+        Scales8<kToken> f;
+        // parts of staging, one a region of the products with V
+        auto part = [&](auto b_c) {
+            constexpr int b = decltype(b_c)::value;
+            if constexpr (last) return;
+            if constexpr (b == 0) stage_k(i, 0);             // tile i + 2 in tile i's buffer
+            if constexpr (b == 1) {
+                if constexpr (F == 2) stage_k(i, 1);
+                load_k(tile(i + 3), p3);
+            }
+            if constexpr (b == 2) stage_v(i + 1, 0);
+            if constexpr (b == 3) {
+                if constexpr (F == 2) stage_v(i + 1, 1);
+                load_v(tile(i + 2), p2);
+                p1 = p2;
+                p2 = p3;
+                p3 = ld.pages(tile(i + 4));
+            }
+        };
+        if constexpr (!last) clean_v(tile(i + 1));
+        if (!busy) {
+            part(IC<0>{});
+            part(IC<1>{});
+            part(IC<2>{});
+            part(IC<3>{});
+            if constexpr (!last) lds_barrier();
+            return;
+        }
         if constexpr (!last) read_k(k, i + 1, 0);
+        const int end = ld.end_key(i) - ld.first_key(i);
+        const bool masked = last && end < kC8Tile;
+        f.set(ks, vs, cs, masked, end, lane);
+        if constexpr (!last) ld.load_scales(ks, vs, i + 1, p1);
+        const int seen[NT] = {end - 1, end - 1};
+        refer8<D, NT, kToken>(r, sc, f, masked, seen, g);
+        // Operands are read one block ahead of their products; the regions keep the compiler from reading them all first.
         auto quarter = [&](auto b_c) {
             constexpr int b = decltype(b_c)::value;
             bf16x8 next[D / 32];
@@ -632,20 +673,32 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
         quarter(IC<2>{});
         quarter(IC<3>{});
         sum8<D, NT, kToken>(r, p, f);
-#pragma unroll
-        for (int b = 0; b < D / 16; ++b) {
+        auto region = [&](auto b_c) {
+            constexpr int b = decltype(b_c)::value;
             bf16x8 next[2];
-            if (b + 1 < D / 16) read_v(next, i, b + 1);
+            if constexpr (b + 1 < D / 16) read_v(next, i, b + 1);
+            part(b_c);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) r.o[n][b] = mfma16(v[u], p[n][u], r.o[n][b]);
-            if (b + 1 < D / 16) {
+            if constexpr (b + 1 < D / 16) {
                 v[0] = next[0];
                 v[1] = next[1];
             }
             __builtin_amdgcn_sched_barrier(0);
+        };
+        region(IC<0>{});
+        region(IC<1>{});
+        region(IC<2>{});
+        region(IC<3>{});
+        if constexpr (D == 128) {
+            region(IC<4>{});
+            region(IC<5>{});
+            region(IC<6>{});
+            region(IC<7>{});
         }
+        if constexpr (!last) lds_barrier();
     };
     for (int i = 0; i + 1 < tiles; ++i) step(std::false_type{}, i);
     step(std::true_type{}, tiles - 1);
