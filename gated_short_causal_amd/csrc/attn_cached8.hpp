@@ -100,9 +100,6 @@ struct Keys8 {
 // product with a page number and the uniform offset.  No branch on the page size:
 // the loads in flight are then counted exactly.  Tokens past the end are read from
 // the last page that exists.
-struct Pages8 {
-    int32_t k, v;            // page numbers: of the lane's keys, of its values
-};
 template <int D, bool kToken>
 struct Loader8 {
     const Cached8Args& a;
@@ -129,35 +126,36 @@ struct Loader8 {
     // groups of 16 tokens of the tile: of the lane's keys, of its values
     __device__ __forceinline__ int key_group() const { return (lane & 15) >> 2; }
     __device__ __forceinline__ int value_group() const { return lane >> 4; }
-    __device__ __forceinline__ Pages8 pages(int i) const {
+    // page numbers: of the lane's keys, of its values
+    __device__ __forceinline__ int32_t key_page(int i) const { return page(i, key_group()); }
+    __device__ __forceinline__ int32_t value_page(int i) const { return page(i, value_group()); }
+    __device__ __forceinline__ int32_t page(int i, int group) const {
         const int32_t* table = is_prefix(i) ? s.prefix : s.own;
-        const int first = first_key(i), last = (end_key(i) - 1) >> shift;
-        return Pages8{table[(uint32_t)min((first + 16 * key_group()) >> shift, last)],
-                      table[(uint32_t)min((first + 16 * value_group()) >> shift, last)]};
+        return table[(uint32_t)min((first_key(i) + 16 * group) >> shift, (end_key(i) - 1) >> shift)];
     }
     __device__ __forceinline__ uint32_t in_page(int i) const { return (uint32_t)(first_key(i) & ((1 << shift) - 1)); }
     __device__ __forceinline__ uint64_t in_pool(int32_t p) const { return (uint32_t)min(max(p, 0), a.c.num_pages - 1); }
-    __device__ __forceinline__ const uint8_t* key_at(int i, const Pages8& p) const {
-        return k + in_pool(p.k) * (uint32_t)a.page_stride + in_page(i) * D;
+    __device__ __forceinline__ const uint8_t* key_at(int i, int32_t p) const {
+        return k + in_pool(p) * (uint32_t)a.page_stride + in_page(i) * D;
     }
-    __device__ __forceinline__ const uint8_t* value_at(int i, const Pages8& p) const {
-        return v + in_pool(p.v) * (uint32_t)a.page_stride + in_page(i) * D;
+    __device__ __forceinline__ const uint8_t* value_at(int i, int32_t p) const {
+        return v + in_pool(p) * (uint32_t)a.page_stride + in_page(i) * D;
     }
-    __device__ __forceinline__ void load_k(Tile8<D>& t, int i, const Pages8& g) const {
-        const uint8_t* p = key_at(i, g);
+    __device__ __forceinline__ void load_k(Tile8<D>& t, int i, int32_t pk) const {
+        const uint8_t* p = key_at(i, pk);
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
             for (int h = 0; h < D / 64; ++h) t.k[b][h] = *reinterpret_cast<const uint4*>(p + 4 * b * D + 16 * h);
     }
-    __device__ __forceinline__ void load_v(Tile8<D>& t, int i, const Pages8& g) const {
-        const uint8_t* p = value_at(i, g);
+    __device__ __forceinline__ void load_v(Tile8<D>& t, int i, int32_t pv) const {
+        const uint8_t* p = value_at(i, pv);
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) t.v[b] = *reinterpret_cast<const uint4*>(p + b * 256);
     }
-    __device__ __forceinline__ void load_scales(float& k1, float& v1, int i, const Pages8& g) const {
+    __device__ __forceinline__ void load_scales(float& k1, float& v1, int i, int32_t pv) const {
         // The offset, a multiple of 64, and the lane's tokens below 64 do not carry into each other's part of the block number.
-        const uint64_t at = in_pool(g.v) * (uint32_t)a.scale_stride + (in_page(i) >> a.block_shift);
+        const uint64_t at = in_pool(pv) * (uint32_t)a.scale_stride + (in_page(i) >> a.block_shift);
         k1 = ks[at];
         v1 = vs[at];
     }
@@ -235,33 +233,34 @@ struct Scales8 {
     }
 };
 
-// The scores of a tile, s[t][i] of key 16 g + 4 t + i, first move the rows'
-// reference where they pass it by 2^kLazy.  masked: keys numbered above seen[n]
-// within the tile are -inf from here on (masked: uniform).
+// The scores of a tile, s[t][i] of key 16 g + 4 t + i: the rows' maxima, times log2 e,
+// of row tile n.  masked (uniform): keys numbered above `seen` within the tile are
+// -inf from here on.
+template <int NT, bool kToken>
+__device__ __forceinline__ float peak8(f32x4 (&s)[NT][4], int n, const Scales8<kToken>& sc, bool masked, int seen, int g) {
+    if constexpr (kToken)
+        for_keys([&](auto i) {
+            constexpr int e = decltype(i)::value;
+            s[n][e >> 2][e & 3] *= row_lane<e>(sc.k);
+        });
+    if (masked) {
+        masked_side();
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+            if (16 * g + e > seen) s[n][e >> 2][e & 3] = kNegInf;
+    }
+    float mx = s[n][0][0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[n][e >> 2][e & 3]);
+    return max_groups(kToken ? mx : mx * sc.k);
+}
+
+// The rows' reference moves where a maximum passes it by 2^kLazy.
 template <int D, int NT, bool kToken>
-__device__ __forceinline__ void refer8(Rows8<D, NT, kToken>& r, f32x4 (&s)[NT][4], const Scales8<kToken>& sc, bool masked,
-                                       const int (&seen)[NT], int g) {
-    float mn[NT];
+__device__ __forceinline__ void refer8(Rows8<D, NT, kToken>& r, const float (&mn)[NT]) {
     bool move = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        if constexpr (kToken)
-            for_keys([&](auto i) {
-                constexpr int e = decltype(i)::value;
-                s[n][e >> 2][e & 3] *= row_lane<e>(sc.k);
-            });
-        if (masked) {
-            masked_side();
-#pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (16 * g + e > seen[n]) s[n][e >> 2][e & 3] = kNegInf;
-        }
-        float mx = s[n][0][0];
-#pragma unroll
-        for (int e = 1; e < 16; ++e) mx = fmaxf(mx, s[n][e >> 2][e & 3]);
-        mn[n] = max_groups(kToken ? mx : mx * sc.k);
-        move |= mn[n] > r.m[n] + kLazy;
-    }
+    for (int n = 0; n < NT; ++n) move |= mn[n] > r.m[n] + kLazy;
     if (__any(move)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -347,7 +346,10 @@ __device__ __forceinline__ void attend8(Rows8<D, NT, kToken>& r, const bf16x8 (&
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) drop_codes(t.v[b], end - 16 * g);
     }
-    refer8<D, NT, kToken>(r, s, sc, masked, seen, g);
+    float mn[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) mn[n] = peak8(s, n, sc, masked, seen[n], g);
+    refer8(r, mn);
     bf16x8 p[NT][2];
     weigh8<0>(r, s, p, sc, [] {});
     weigh8<1>(r, s, p, sc, [] {});
@@ -376,11 +378,14 @@ __device__ __forceinline__ void walk8(Rows8<D, NT, kToken>& r, const bf16x8 (&q)
     const Loader8<D, kToken> ld(a, s, kvh, lane);
     const float cs = a.c.scale * kLog2e;
     Tile8<D> t;
-    Pages8 now = ld.pages(mine), ahead{0, 0};
-    ld.load_k(t, mine, now);
-    ld.load_scales(t.ks, t.vs, mine, now);
-    ld.load_v(t, mine, now);
-    if (mine + step < tiles) ahead = ld.pages(mine + step);
+    int32_t nk = ld.key_page(mine), nv = ld.value_page(mine);        // page numbers of the tile that is loaded next
+    ld.load_k(t, mine, nk);
+    ld.load_scales(t.ks, t.vs, mine, nv);
+    ld.load_v(t, mine, nv);
+    if (mine + step < tiles) {
+        nk = ld.key_page(mine + step);
+        nv = ld.value_page(mine + step);
+    }
     for (int i = mine; i < tiles; i += step) {
         const bool prefix = ld.is_prefix(i);
         const int k0 = ld.first_key(i), end = ld.end_key(i) - k0;
@@ -390,13 +395,14 @@ __device__ __forceinline__ void walk8(Rows8<D, NT, kToken>& r, const bf16x8 (&q)
         const int next = i + step;
         auto after_k = [&] {
             if (next >= tiles) return;
-            now = ahead;
-            ahead = ld.pages(min(next + step, tiles - 1));
-            ld.load_k(t, next, now);
-            ld.load_scales(t.ks, t.vs, next, now);
+            ld.load_k(t, next, nk);
+            nk = ld.key_page(min(next + step, tiles - 1));
+            ld.load_scales(t.ks, t.vs, next, nv);
         };
         auto after_v = [&] {
-            if (next < tiles) ld.load_v(t, next, now);
+            if (next >= tiles) return;
+            ld.load_v(t, next, nv);
+            nv = ld.value_page(min(next + step, tiles - 1));
         };
         const bool masked = prefix ? end < kC8Tile : k0 + kC8Tile - 1 > least;
         attend8<D, NT, kInt8, kToken>(r, q, t, cs, masked, seen, end, lane, after_k, after_v);
@@ -546,10 +552,10 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
     Codes kc, vc;                                        // codes of K and V on their way to LDS
     float ks, vs;
     auto tile = [&](int i) { return min(i, tiles - 1); };
-    auto load_k = [&](int i, const Pages8& p) {
+    auto load_k = [&](int i, int32_t p) {
         kc = *reinterpret_cast<const Codes*>(ld.key_at(i, p) + 4 * kb * D + (D / 8) * kh);
     };
-    auto load_v = [&](int i, const Pages8& p) { vc = *reinterpret_cast<const Codes*>(ld.value_at(i, p) + 256 * vb + 8 * vh); };
+    auto load_v = [&](int i, int32_t p) { vc = *reinterpret_cast<const Codes*>(ld.value_at(i, p) + 256 * vb + 8 * vh); };
     auto operand = [&](const Codes& x, int u) {
         if constexpr (D == 128) return __builtin_bit_cast(uint4, u ? codes_to_bf16<kInt8>(x.z, x.w) : codes_to_bf16<kInt8>(x.x, x.y));
         else return __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(x.x, x.y));
@@ -585,28 +591,33 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
 #pragma unroll
             for (int n = 0; n < NT; ++n) sc[n][b] = mfma16(k[d], q[n][d], sc[n][b]);
     };
-    // Before step i: the scores and scales of tile i, the codes of K in tile i + 2 and of V in tile i + 1, and the page
-    // numbers of tiles i + 1 to i + 3 are in registers; K of tile i + 1 and V of tile i are staged.  Tiles past the last
-    // are the last once more.
-    Pages8 p1 = ld.pages(0), p2 = ld.pages(tile(1)), p3 = ld.pages(tile(2));
-    load_k(0, p1);
-    load_v(0, p1);
-    ld.load_scales(ks, vs, 0, p1);
+    // Before step i: the scores of tile i with their maxima, its scales and those of tile i + 1, the codes of K in tile
+    // i + 2 and of V in tile i + 1, and the page numbers of K in tile i + 3 and of V in tile
+    // i + 2 are in registers; K of tile i + 1 and V of
+    // tile i are staged.  Tiles past the last are the last once more.
+    const int32_t k0 = ld.key_page(0), k1 = ld.key_page(tile(1)), k2 = ld.key_page(tile(2)), v0 = ld.value_page(0),
+                  v1 = ld.value_page(tile(1));
+    int32_t nk = ld.key_page(tile(3)), nv = ld.value_page(tile(2));
+    Scales8<kToken> f;
+    load_k(0, k0);
+    load_v(0, v0);
+    ld.load_scales(ks, vs, 0, v0);
 #pragma unroll
     for (int u = 0; u < F; ++u) stage_k(0, u);
-    load_k(tile(1), p2);
+    load_k(tile(1), k1);
     clean_v(0);
 #pragma unroll
     for (int u = 0; u < F; ++u) stage_v(0, u);
-    load_v(tile(1), p2);
+    load_v(tile(1), v1);
 #pragma unroll
     for (int u = 0; u < F; ++u) stage_k(1, u);
-    load_k(tile(2), p3);
-    p1 = p2;
-    p2 = p3;
-    p3 = ld.pages(tile(3));
+    load_k(tile(2), k2);
+    int end = min(ld.end_key(0) - ld.first_key(0), kC8Tile);         // keys of the tile
+    f.set(ks, vs, cs, end < kC8Tile, end, lane);
+    ld.load_scales(ks, vs, tile(1), v1);
     lds_barrier();
     f32x4 sc[NT][4];
+    float mn[NT];
     if (busy) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
@@ -614,56 +625,70 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
             read_k(k, 0, b);
             products(sc, k, b);
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) mn[n] = peak8(sc, n, f, end < kC8Tile, end - 1, g);
     }
     lds_barrier();                                       // K of tile 0 is read: its buffer takes tile 2
-    auto step = [&](auto last_c, int i) {
-        constexpr bool last = decltype(last_c)::value;       // the part may end within its last tile
+    // kMore: tiles that follow, 2 for two or more; only the last may end within the tile.
+    // busy_c: the wave has rows.  The others only stage, in a loop of their own: in one with both, the compiler would wait
+    // for either's loads.
+    auto step = [&](auto busy_c, auto more_c, int i) {
+        constexpr int kMore = decltype(more_c)::value;
+        constexpr bool has = decltype(busy_c)::value;
         bf16x8 p[NT][2], k[D / 32], v[2];
-        Scales8<kToken> f;
-        // parts of staging, one a region of the products with V
+        Scales8<kToken> g1;
+        float m1[NT];
+        if constexpr (kMore == 1) {
+            end = min(ld.end_key(i + 1) - ld.first_key(i + 1), kC8Tile);
+            clean_v(i + 1);
+        }
+        // What is done beside the product with V: one part a region.  A register is loaded in a later region than its last
+        // use: in the same one the compiler may load first, into another register, and wait for the load to copy it.
         auto part = [&](auto b_c) {
-            constexpr int b = decltype(b_c)::value;
-            if constexpr (last) return;
+            constexpr int b = D == 128 ? decltype(b_c)::value : 2 * decltype(b_c)::value;
+            const bool masked = kMore == 1 && end < kC8Tile;
+            if constexpr (kMore == 0) return;
             if constexpr (b == 0) stage_k(i, 0);             // tile i + 2 in tile i's buffer
-            if constexpr (b == 1) {
-                if constexpr (F == 2) stage_k(i, 1);
-                load_k(tile(i + 3), p3);
+            if constexpr (b == 1) stage_k(i, 1);
+            if constexpr (b == 2) {
+                load_k(tile(i + 3), nk);
+                stage_v(i + 1, 0);
             }
-            if constexpr (b == 2) stage_v(i + 1, 0);
-            if constexpr (b == 3) {
-                if constexpr (F == 2) stage_v(i + 1, 1);
-                load_v(tile(i + 2), p2);
-                p1 = p2;
-                p2 = p3;
-                p3 = ld.pages(tile(i + 4));
+            if constexpr (b == 3) stage_v(i + 1, 1);
+            if constexpr (b == 4) {
+                nk = ld.key_page(tile(i + 4));
+                load_v(tile(i + 2), nv);
+                g1.set(ks, vs, cs, masked, end, lane);
+            }
+            if constexpr (b == 6) {
+                ld.load_scales(ks, vs, tile(i + 2), nv);
+                if constexpr (has) m1[0] = peak8(sc, 0, g1, masked, end - 1, g);
+            }
+            if constexpr (b == (D == 128 ? 7 : 6)) {
+                if (D == 64) __builtin_amdgcn_sched_barrier(0);
+                nv = ld.value_page(tile(i + 3));
+                if constexpr (has) m1[1] = peak8(sc, 1, g1, masked, end - 1, g);
             }
         };
-        if constexpr (!last) clean_v(tile(i + 1));
-        if (!busy) {
-            part(IC<0>{});
-            part(IC<1>{});
-            part(IC<2>{});
-            part(IC<3>{});
-            if constexpr (!last) lds_barrier();
+        auto parts = [&](auto... b) { (part(b), ...); };
+        if constexpr (!has) {
+            if constexpr (D == 128) parts(IC<0>{}, IC<1>{}, IC<2>{}, IC<3>{}, IC<4>{}, IC<6>{}, IC<7>{});
+            else parts(IC<0>{}, IC<1>{}, IC<2>{}, IC<3>{});
+            if constexpr (kMore > 0) lds_barrier();
             return;
         }
-        if constexpr (!last) read_k(k, i + 1, 0);
-        const int end = ld.end_key(i) - ld.first_key(i);
-        const bool masked = last && end < kC8Tile;
-        f.set(ks, vs, cs, masked, end, lane);
-        if constexpr (!last) ld.load_scales(ks, vs, i + 1, p1);
-        const int seen[NT] = {end - 1, end - 1};
-        refer8<D, NT, kToken>(r, sc, f, masked, seen, g);
+        if constexpr (kMore > 0) read_k(k, i + 1, 0);
+        refer8(r, mn);
         // Operands are read one block ahead of their products; the regions keep the compiler from reading them all first.
         auto quarter = [&](auto b_c) {
             constexpr int b = decltype(b_c)::value;
             bf16x8 next[D / 32];
-            if constexpr (!last && b < 3) read_k(next, i + 1, b + 1);
+            if constexpr (kMore > 0 && b < 3) read_k(next, i + 1, b + 1);
             if constexpr (b == 3) read_v(v, i, 0);
             weigh8<b>(r, sc, p, f, [&] {
-                if constexpr (!last) products(sc, k, b);
+                if constexpr (kMore > 0) products(sc, k, b);
             });
-            if constexpr (!last && b < 3)
+            if constexpr (kMore > 0 && b < 3)
 #pragma unroll
                 for (int d = 0; d < D / 32; ++d) k[d] = next[d];
             __builtin_amdgcn_sched_barrier(0);
@@ -698,14 +723,27 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
             region(IC<6>{});
             region(IC<7>{});
         }
-        if constexpr (!last) lds_barrier();
+        if constexpr (kMore > 0) {
+            f = g1;
+            mn[0] = m1[0];
+            mn[1] = m1[1];
+            lds_barrier();
+        }
     };
-    for (int i = 0; i + 1 < tiles; ++i) step(std::false_type{}, i);
-    step(std::true_type{}, tiles - 1);
+    auto walk = [&](auto busy_c) {
+        for (int i = 0; i + 2 < tiles; ++i) step(busy_c, IC<2>{}, i);
+        if (tiles > 1) step(busy_c, IC<1>{}, tiles - 2);
+        step(busy_c, IC<0>{}, tiles - 1);
+    };
+    if (!busy) {
+        walk(std::false_type{});
+        return;
+    }
+    walk(std::true_type{});
     float l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) l[n] = r.sum(n);
-    if (busy) store8<D, NT, kToken>(ca, r, l, kvh, x0, rows, split, false, lane);
+    store8<D, NT, kToken>(ca, r, l, kvh, x0, rows, split, false, lane);
 }
 
 // Forms of a call (see cached8_plan).
