@@ -1,5 +1,7 @@
 // attn_cached8.hip -- plan and dispatch of the attention over a paged cache of
 // 8-bit codes (attn_cached8.hpp).
+#include <algorithm>
+
 #include "attn_cached8.hpp"
 
 namespace lfm2sc {
@@ -13,8 +15,8 @@ Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, i
     p.prefix_splits = 0;
     p.prefix_chunk = 0;
     p.prefix_blocks = 0;
-    p.form = base <= 256 && ptiles + otiles <= 2 * form_waves(kDirect8) ? kDirect8
-             : prefix_len > 0 && rows > 64                              ? kShared8
+    p.form = base <= 512 && ptiles + otiles <= (base >= 128 ? 32 : 16) ? kDirect8
+             : prefix_len > 0 && rows > kSharedRows                              ? kShared8
                                                                         : kSplit8;
     if (p.form == kDirect8) {
         p.suffix_splits = 0;
@@ -23,15 +25,18 @@ Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, i
     }
     if (prefix_len > 0) {
         const int64_t rows_wg = p.form == kShared8 ? kSharedRows : rows_unit, row_blocks = (rows + rows_wg - 1) / rows_wg;
-        const int64_t want = (p.form == kShared8 ? 256 : 1024) / (row_blocks * Hkv);
-        const int64_t most = p.form == kShared8 ? (ptiles + 3) / 4 : (ptiles + 3) / 4;
+        // seconds at 8e14 flops/s and 5e12 bytes/s; a batch fills about half of its longest suffix
+        const double product = 4. * rows * Hkv * D * prefix_len / 8e14, read = (double)N * max_suffix * Hkv * D / 5e12;
+        const double share = product / (product + read);
+        const double slots = p.form == kShared8 ? 256. * form_per_simd(D, 1, kShared8) * (share > 0.8 ? 1. : share) : 256.;
+        const int64_t want = (int64_t)(slots / (double)(row_blocks * Hkv)), most = (ptiles + 3) / 4;
         const int64_t splits = want < 1 ? 1 : want < most ? want : most;
         const int64_t per = (ptiles + splits - 1) / splits;
         p.prefix_chunk = (int)per * kC8Tile;
         p.prefix_splits = (int)((ptiles + per - 1) / per);
         p.prefix_blocks = row_blocks * Hkv * p.prefix_splits;
     }
-    const int64_t most = (otiles + 3) / 4, want = 2048 / base;
+    const int64_t most = (otiles + 3) / 4, want = std::min<int64_t>((rows_unit == 16 ? 2048 : 1024) / base, 32);
     p.suffix_splits = (int)(want < 1 ? 1 : want < most ? want : most);
     if (p.suffix_splits < 1) p.suffix_splits = 1;
     const int per_wg = form_waves(p.form) / own_waves(p.form);

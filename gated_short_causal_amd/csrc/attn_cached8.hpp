@@ -515,14 +515,14 @@ __device__ __forceinline__ void keys8(const Cached8Args& a, const Keys8& s, int 
     if (wave == 0) store8<D, NT, kToken>(ca, r, l, kvh, x0, rows, split, whole, lane);
 }
 
-// Prefix keys for many rows: 8 waves of 32 query rows share each tile.  They turn
+// Prefix keys for many rows: 4 waves of 32 query rows share each tile.  They turn
 // its codes into bf16 operands once, in LDS in the order in which the products
 // read them (operand, lane: 16 bytes each, no bank conflict), two buffers of K and
-// of V, one barrier a tile.  With two waves a SIMD the vector unit has to work
-// beside the matrix unit within a wave: between two barriers the scores of tile i
+// of V, one barrier a tile.  With two or three waves a SIMD the vector unit has to
+// work beside the matrix unit within a wave: between two barriers the scores of tile i
 // turn into p while those of tile i + 1 are formed, and the codes of K in tile
 // i + 2 and of V in tile i + 1 are staged while p V is added up.
-constexpr int kSharedRows = 32 * 8;
+constexpr int kSharedRows = 32 * 4;
 template <int D>
 constexpr int shared_bytes() { return 4 * kC8Tile * D * 2; }
 template <int D, bool kInt8, bool kToken>
@@ -544,35 +544,30 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
     const int tiles = s.ptiles;
     Rows8<D, NT, kToken> r;
     r.clear();
-    // Wave w brings, of block w >> 1 of the keys, half w & 1 of a lane's codes (D = 128: 16 of them, D = 64: 8), and of V
-    // channels 16 w .. (D = 128), or 8 of a lane's 16 tokens of channels 16 (w >> 1) .. (D = 64).
-    constexpr int F = D / 64;                            // operands of a wave, of K and of V
-    using Codes = std::conditional_t<D == 128, uint4, uint2>;
-    const int kb = wave >> 1, kh = wave & 1, vb = D == 128 ? wave : wave >> 1, vh = D == 128 ? 0 : wave & 1;
-    Codes kc, vc;                                        // codes of K and V on their way to LDS
+    // Wave w brings block w of the keys, and of V channels D / 4 w ..; C times 16 codes a lane of each, 2 C operands.
+    constexpr int C = D / 64;
+    uint4 kc[C], vc[C];                                  // codes of K and V on their way to LDS
     float ks, vs;
     auto tile = [&](int i) { return min(i, tiles - 1); };
     auto load_k = [&](int i, int32_t p) {
-        kc = *reinterpret_cast<const Codes*>(ld.key_at(i, p) + 4 * kb * D + (D / 8) * kh);
+#pragma unroll
+        for (int h = 0; h < C; ++h) kc[h] = *reinterpret_cast<const uint4*>(ld.key_at(i, p) + 4 * wave * D + 16 * h);
     };
-    auto load_v = [&](int i, int32_t p) { vc = *reinterpret_cast<const Codes*>(ld.value_at(i, p) + 256 * vb + 8 * vh); };
-    auto operand = [&](const Codes& x, int u) {
-        if constexpr (D == 128) return __builtin_bit_cast(uint4, u ? codes_to_bf16<kInt8>(x.z, x.w) : codes_to_bf16<kInt8>(x.x, x.y));
-        else return __builtin_bit_cast(uint4, codes_to_bf16<kInt8>(x.x, x.y));
+    auto load_v = [&](int i, int32_t p) {
+#pragma unroll
+        for (int h = 0; h < C; ++h) vc[h] = *reinterpret_cast<const uint4*>(ld.value_at(i, p) + 256 * (C * wave + h));
     };
-    auto stage_k = [&](int i, int u) { lds[(i & 1) * kBuf + (kb * (D / 32) + F * kh + u) * 64 + lane] = operand(kc, u); };
-    auto stage_v = [&](int i, int u) { lds[(2 + (i & 1)) * kBuf + (vb * 2 + vh + u) * 64 + lane] = operand(vc, u); };
+    auto operand = [&](const uint4& x, int u) {
+        return __builtin_bit_cast(uint4, u ? codes_to_bf16<kInt8>(x.z, x.w) : codes_to_bf16<kInt8>(x.x, x.y));
+    };
+    auto stage_k = [&](int i, int u) { lds[(i & 1) * kBuf + (2 * C * wave + u) * 64 + lane] = operand(kc[u >> 1], u & 1); };
+    auto stage_v = [&](int i, int u) { lds[(2 + (i & 1)) * kBuf + (2 * C * wave + u) * 64 + lane] = operand(vc[u >> 1], u & 1); };
     auto clean_v = [&](int i) {                          // e4m3: no NaN from tokens that do not exist
         const int end = ld.end_key(i) - ld.first_key(i);
         if (!kInt8 && end < kC8Tile) {
             masked_side();
-            if constexpr (D == 128) {
-                drop_codes(vc, end - 16 * g);
-            } else {
-                uint4 x = make_uint4(vc.x, vc.y, 0, 0);
-                drop_codes(x, end - 16 * g - 8 * vh);
-                vc = make_uint2(x.x, x.y);
-            }
+#pragma unroll
+            for (int h = 0; h < C; ++h) drop_codes(vc[h], end - 16 * g);
         }
     };
     auto read_k = [&](bf16x8 (&k)[D / 32], int i, int b) {
@@ -603,14 +598,14 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
     load_v(0, v0);
     ld.load_scales(ks, vs, 0, v0);
 #pragma unroll
-    for (int u = 0; u < F; ++u) stage_k(0, u);
+    for (int u = 0; u < 2 * C; ++u) stage_k(0, u);
     load_k(tile(1), k1);
     clean_v(0);
 #pragma unroll
-    for (int u = 0; u < F; ++u) stage_v(0, u);
+    for (int u = 0; u < 2 * C; ++u) stage_v(0, u);
     load_v(tile(1), v1);
 #pragma unroll
-    for (int u = 0; u < F; ++u) stage_k(1, u);
+    for (int u = 0; u < 2 * C; ++u) stage_k(1, u);
     load_k(tile(2), k2);
     int end = min(ld.end_key(0) - ld.first_key(0), kC8Tile);         // keys of the tile
     f.set(ks, vs, cs, end < kC8Tile, end, lane);
@@ -635,7 +630,7 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
     auto step = [&](auto busy_c, auto more_c, int i) {
         constexpr int kMore = decltype(more_c)::value;
         constexpr bool has = decltype(busy_c)::value;
-        bf16x8 p[NT][2], k[D / 32], v[2];
+        bf16x8 p[NT][2], k[D / 32], v[2], w[2];
         Scales8<kToken> g1;
         float m1[NT];
         if constexpr (kMore == 1) {
@@ -645,46 +640,49 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
         // What is done beside the product with V: one part a region.  A register is loaded in a later region than its last
         // use: in the same one the compiler may load first, into another register, and wait for the load to copy it.
         auto part = [&](auto b_c) {
-            constexpr int b = D == 128 ? decltype(b_c)::value : 2 * decltype(b_c)::value;
+            constexpr int b = decltype(b_c)::value, q = D / 64;      // q regions for each of four parts
             const bool masked = kMore == 1 && end < kC8Tile;
             if constexpr (kMore == 0) return;
-            if constexpr (b == 0) stage_k(i, 0);             // tile i + 2 in tile i's buffer
-            if constexpr (b == 1) stage_k(i, 1);
-            if constexpr (b == 2) {
-                load_k(tile(i + 3), nk);
-                stage_v(i + 1, 0);
+            if constexpr (b < q) {                           // tile i + 2 in tile i's buffer
+                stage_k(i, 2 * b);
+                stage_k(i, 2 * b + 1);
             }
-            if constexpr (b == 3) stage_v(i + 1, 1);
-            if constexpr (b == 4) {
+            if constexpr (b == q) load_k(tile(i + 3), nk);
+            if constexpr (b >= q && b < 2 * q) {
+                stage_v(i + 1, 2 * (b - q));
+                stage_v(i + 1, 2 * (b - q) + 1);
+            }
+            if constexpr (b == 2 * q) {
                 nk = ld.key_page(tile(i + 4));
                 load_v(tile(i + 2), nv);
                 g1.set(ks, vs, cs, masked, end, lane);
             }
-            if constexpr (b == 6) {
+            if constexpr (b == 3 * q) {
                 ld.load_scales(ks, vs, tile(i + 2), nv);
                 if constexpr (has) m1[0] = peak8(sc, 0, g1, masked, end - 1, g);
             }
-            if constexpr (b == (D == 128 ? 7 : 6)) {
-                if (D == 64) __builtin_amdgcn_sched_barrier(0);
+            if constexpr (b == 4 * q - 1) {
+                if (q == 1) __builtin_amdgcn_sched_barrier(0);
                 nv = ld.value_page(tile(i + 3));
                 if constexpr (has) m1[1] = peak8(sc, 1, g1, masked, end - 1, g);
             }
         };
         auto parts = [&](auto... b) { (part(b), ...); };
         if constexpr (!has) {
-            if constexpr (D == 128) parts(IC<0>{}, IC<1>{}, IC<2>{}, IC<3>{}, IC<4>{}, IC<6>{}, IC<7>{});
+            if constexpr (D == 128) parts(IC<0>{}, IC<1>{}, IC<2>{}, IC<3>{}, IC<4>{}, IC<5>{}, IC<6>{}, IC<7>{});
             else parts(IC<0>{}, IC<1>{}, IC<2>{}, IC<3>{});
             if constexpr (kMore > 0) lds_barrier();
             return;
         }
         if constexpr (kMore > 0) read_k(k, i + 1, 0);
         refer8(r, mn);
-        // Operands are read one block ahead of their products; the regions keep the compiler from reading them all first.
+        // Operands are read a block (of K) or two (of V) ahead of their products; the regions keep the compiler from reading them all first.
         auto quarter = [&](auto b_c) {
             constexpr int b = decltype(b_c)::value;
             bf16x8 next[D / 32];
             if constexpr (kMore > 0 && b < 3) read_k(next, i + 1, b + 1);
-            if constexpr (b == 3) read_v(v, i, 0);
+            if constexpr (b == 2) read_v(v, i, 0);
+            if constexpr (b == 3) read_v(w, i, 1);
             weigh8<b>(r, sc, p, f, [&] {
                 if constexpr (kMore > 0) products(sc, k, b);
             });
@@ -701,15 +699,16 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
         auto region = [&](auto b_c) {
             constexpr int b = decltype(b_c)::value;
             bf16x8 next[2];
-            if constexpr (b + 1 < D / 16) read_v(next, i, b + 1);
+            if constexpr (b + 2 < D / 16) read_v(next, i, b + 2);
             part(b_c);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) r.o[n][b] = mfma16(v[u], p[n][u], r.o[n][b]);
-            if constexpr (b + 1 < D / 16) {
-                v[0] = next[0];
-                v[1] = next[1];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                v[u] = w[u];
+                if constexpr (b + 2 < D / 16) w[u] = next[u];
             }
             __builtin_amdgcn_sched_barrier(0);
         };
@@ -749,21 +748,21 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
 // Forms of a call (see cached8_plan).
 //   kDirect  a workgroup of 8 waves reads prefix and suffix of its rows and writes the output
 //   kSplit   workgroups of 4 waves, the prefix's first (few rows), then the suffixes'
-//   kShared  workgroups of 8 waves: the prefix's (many rows, shared8), then two units of 4 waves of the suffixes
+//   kShared  workgroups of 4 waves: the prefix's (many rows, shared8), then four units of a wave each of the suffixes
 enum Form8 { kDirect8, kSplit8, kShared8 };
-constexpr int form_waves(int form) { return form == kSplit8 ? 4 : 8; }
+constexpr int form_waves(int form) { return form == kDirect8 ? 8 : 4; }
 // waves a SIMD, which bounds their registers: 128, 168 or 256 of 512
 constexpr int form_per_simd(int D, int NT, int form) {
-    if (D == 64 && NT == 1) return form == kShared8 ? 2 : 4;
-    return form == kSplit8 && (D == 64 || NT == 1) ? 3 : 2;
+    if (D == 128) return 2;
+    if (form == kSplit8) return NT == 1 ? 4 : 3;
+    return form == kShared8 ? 3 : NT == 1 ? 4 : 2;
 }
-constexpr int own_waves(int form) { return form == kDirect8 ? 8 : 4; }
+constexpr int own_waves(int form) { return form == kDirect8 ? 8 : form == kSplit8 ? 4 : 1; }
 
 template <int D, int NT, bool kInt8, bool kToken, int kForm>
 __global__ __launch_bounds__(64 * form_waves(kForm), form_per_simd(D, NT, kForm)) void attn_cached8_kernel(Cached8Args a) {
     constexpr int W = form_waves(kForm), U = own_waves(kForm);
-    constexpr int kJoin = W / 2 * join_floats<D, NT>() * 4;
-    constexpr int kLds = kForm == kShared8 && shared_bytes<D>() > kJoin ? shared_bytes<D>() : kJoin;
+    constexpr int kLds = kForm == kShared8 ? shared_bytes<D>() : W / 2 * join_floats<D, NT>() * 4;
     __shared__ uint4 lds[kLds / 16];
     const CachedArgs& ca = a.c;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
