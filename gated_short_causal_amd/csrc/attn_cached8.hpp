@@ -53,16 +53,11 @@ __device__ __forceinline__ bf16x8 codes_to_bf16(uint32_t lo, uint32_t hi) {
     return r.v;
 }
 
-// Maximum and sum over the four lanes of a column (16 apart).
+// Maximum over the four lanes of a column (16 apart).
 __device__ __forceinline__ float max_groups(float x) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
     return max_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
 }
-__device__ __forceinline__ float sum_groups(float x) {
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-    return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
-}
-
 // The value of lane i of the lane's row of 16.
 template <int i>
 __device__ __forceinline__ float row_lane(float x) {
@@ -162,30 +157,27 @@ struct Loader8 {
 };
 
 // Running softmax state of 16 NT query rows (row 16 n + c): reference m, sum l and
-// output o, relative to 2^m.  kToken: l is the sum of the lane's own keys.  Else l is
-// a result of the matrix unit like o, with a value 1 / vs in place of a channel's
-// code (rows 0 and 1: its two bf16 parts), because p carries vs: the sum costs
-// nothing of the vector unit, which bounds the kernel where many rows share a tile.
-template <int D, int NT, bool kToken>
+// output o, relative to 2^m.  l is a result of the matrix unit like o, with 1 / vs in
+// place of a channel's code (rows 0 and 1: its two bf16 parts, 2^-17 of it off),
+// because p carries vs: so it adds up the very p that o does, rounded, which takes
+// most of that rounding out of o / l (1.9e-3 of an output off, 2.4e-3 with a sum of
+// unrounded p), and costs nothing of the vector unit, which bounds the kernel where
+// many rows share a tile.
+template <int D, int NT>
 struct Rows8 {
-    using Sum = std::conditional_t<kToken, float, f32x4>;
     float m[NT];
-    Sum l[NT];
-    f32x4 o[NT][D / 16];
+    f32x4 l[NT], o[NT][D / 16];
     __device__ void clear() {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             m[n] = kNegInf;
-            l[n] = Sum{};
+            l[n] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int b = 0; b < D / 16; ++b) o[n][b] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
     }
     // the row's sum, in all of its lanes
-    __device__ __forceinline__ float sum(int n) const {
-        if constexpr (kToken) return sum_groups(l[n]);
-        else return __shfl(l[n][0] + l[n][1], threadIdx.x & 15, 64);
-    }
+    __device__ __forceinline__ float sum(int n) const { return __shfl(l[n][0] + l[n][1], threadIdx.x & 15, 64); }
 };
 
 // Scales as the kernels take them.  A scale below 2^-100 (0: a block of zeros)
@@ -216,19 +208,17 @@ __device__ __forceinline__ void drop_codes(uint4& v, int have) {
 template <bool kToken>
 struct Scales8 {
     float k, v;
-    float log_v;                 // else: log2 v, and 1 / v as the operand of l
-    bf16x8 one;
+    float log_v;                 // not kToken: log2 v,
+    uint32_t one;                // and two values of the operand of l
     __device__ __forceinline__ void set(float ks, float vs, float cs, bool masked, int end, int lane) {
         if (masked) drop_scales<kToken>(ks, vs, end, lane);
-        k = (kToken ? ks : usable(ks)) * cs;
-        v = vs;
+        k = usable(ks) * cs;
+        v = usable(vs);
         if constexpr (!kToken) {
-            v = usable(vs);
             log_v = __builtin_amdgcn_logf(v);
             const float r = __builtin_amdgcn_rcpf(v), hi = __uint_as_float(__float_as_uint(r) & 0xffff0000u);
             const int c = lane & 15;
-            const uint32_t one1 = c < 2 ? Elem<uint16_t>::pack2(c ? r - hi : hi, c ? r - hi : hi) : 0u;
-            one = __builtin_bit_cast(bf16x8, make_uint4(one1, one1, one1, one1));
+            one = c < 2 ? Elem<uint16_t>::pack2(c ? r - hi : hi, c ? r - hi : hi) : 0u;
         }
     }
 };
@@ -256,8 +246,8 @@ __device__ __forceinline__ float peak8(f32x4 (&s)[NT][4], int n, const Scales8<k
 }
 
 // The rows' reference moves where a maximum passes it by 2^kLazy.
-template <int D, int NT, bool kToken>
-__device__ __forceinline__ void refer8(Rows8<D, NT, kToken>& r, const float (&mn)[NT]) {
+template <int D, int NT>
+__device__ __forceinline__ void refer8(Rows8<D, NT>& r, const float (&mn)[NT]) {
     bool move = false;
 #pragma unroll
     for (int n = 0; n < NT; ++n) move |= mn[n] > r.m[n] + kLazy;
@@ -278,7 +268,7 @@ __device__ __forceinline__ void refer8(Rows8<D, NT, kToken>& r, const float (&mn
 // 2 (b & 1) and + 1 of operand b >> 1 of the second product.  between() runs when
 // the scores have been read.
 template <int b, int D, int NT, bool kToken, typename F>
-__device__ __forceinline__ void weigh8(Rows8<D, NT, kToken>& r, f32x4 (&s)[NT][4], bf16x8 (&p)[NT][2], const Scales8<kToken>& sc, F between) {
+__device__ __forceinline__ void weigh8(Rows8<D, NT>& r, f32x4 (&s)[NT][4], bf16x8 (&p)[NT][2], const Scales8<kToken>& sc, F between) {
     float x[NT][4];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -293,7 +283,6 @@ __device__ __forceinline__ void weigh8(Rows8<D, NT, kToken>& r, f32x4 (&s)[NT][4
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[n][i] = exp2_fast(x[n][i]);
         if constexpr (kToken) {
-            r.l[n] += (x[n][0] + x[n][1]) + (x[n][2] + x[n][3]);
             x[n][0] *= row_lane<4 * b>(sc.v);
             x[n][1] *= row_lane<4 * b + 1>(sc.v);
             x[n][2] *= row_lane<4 * b + 2>(sc.v);
@@ -307,19 +296,36 @@ __device__ __forceinline__ void weigh8(Rows8<D, NT, kToken>& r, f32x4 (&s)[NT][4
     }
 }
 
-// l of a block-scaled row.
+// Adds a tile's p to the rows' sums.  The operand: 1 / v of keys 16 g + 8 u + j, of
+// which row 0 (lanes c = 0) holds the upper 8 digits and row 1 the next, the others 0.
 template <int D, int NT, bool kToken>
-__device__ __forceinline__ void sum8(Rows8<D, NT, kToken>& r, const bf16x8 (&p)[NT][2], const Scales8<kToken>& sc) {
-    if constexpr (!kToken)
+__device__ __forceinline__ void sum8(Rows8<D, NT>& r, const bf16x8 (&p)[NT][2], const Scales8<kToken>& sc, int lane) {
+    bf16x8 x[2];
+    if constexpr (kToken) {
+        const float one = __builtin_amdgcn_rcpf(sc.v), hi = __uint_as_float(__float_as_uint(one) & 0xffff0000u);
+        const int c = lane & 15;
+        const float both = __uint_as_float(__float_as_uint(hi) | bf16_bits(one - hi));       // of key 16 g + c
+        const uint32_t pick = c == 0 ? 0x07060302u : c == 1 ? 0x05040100u : 0x0c0c0c0cu;     // halves of two keys', or zeros
+        uint32_t w[8];
+        for_keys([&](auto i) {
+            constexpr int e = decltype(i)::value;
+            if constexpr (e % 2 == 0)
+                w[e / 2] = __builtin_amdgcn_perm(__float_as_uint(row_lane<(e + 1) % 16>(both)), __float_as_uint(row_lane<e>(both)), pick);
+        });
+        x[0] = __builtin_bit_cast(bf16x8, make_uint4(w[0], w[1], w[2], w[3]));
+        x[1] = __builtin_bit_cast(bf16x8, make_uint4(w[4], w[5], w[6], w[7]));
+    } else {
+        x[0] = x[1] = __builtin_bit_cast(bf16x8, make_uint4(sc.one, sc.one, sc.one, sc.one));
+    }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) r.l[n] = mfma16(sc.one, p[n][u], r.l[n]);
+        for (int u = 0; u < 2; ++u) r.l[n] = mfma16(x[u], p[n][u], r.l[n]);
 }
 
 // One tile, in registers, against the wave's rows.
 template <int D, int NT, bool kInt8, bool kToken, typename F1, typename F2>
-__device__ __forceinline__ void attend8(Rows8<D, NT, kToken>& r, const bf16x8 (&q)[NT][D / 32], Tile8<D>& t, float cs, bool masked,
+__device__ __forceinline__ void attend8(Rows8<D, NT>& r, const bf16x8 (&q)[NT][D / 32], Tile8<D>& t, float cs, bool masked,
                                         const int (&seen)[NT], int end, int lane, F1 after_k, F2 after_v) {
     const int g = lane >> 4;
     f32x4 s[NT][4];
@@ -355,7 +361,7 @@ __device__ __forceinline__ void attend8(Rows8<D, NT, kToken>& r, const bf16x8 (&
     weigh8<1>(r, s, p, sc, [] {});
     weigh8<2>(r, s, p, sc, [] {});
     weigh8<3>(r, s, p, sc, [] {});
-    sum8<D, NT, kToken>(r, p, sc);
+    sum8(r, p, sc, lane);
 #pragma unroll
     for (int b = 0; b < D / 16; ++b) {
         const bf16x8 v0 = codes_to_bf16<kInt8>(t.v[b].x, t.v[b].y), v1 = codes_to_bf16<kInt8>(t.v[b].z, t.v[b].w);
@@ -372,7 +378,7 @@ __device__ __forceinline__ void attend8(Rows8<D, NT, kToken>& r, const bf16x8 (&
 // is loaded as soon as the scores are formed, its V after the products, its page
 // numbers a tile earlier.
 template <int D, int NT, bool kInt8, bool kToken>
-__device__ __forceinline__ void walk8(Rows8<D, NT, kToken>& r, const bf16x8 (&q)[NT][D / 32], const Cached8Args& a, const Keys8& s,
+__device__ __forceinline__ void walk8(Rows8<D, NT>& r, const bf16x8 (&q)[NT][D / 32], const Cached8Args& a, const Keys8& s,
                                       int kvh, int tiles, int mine, int step, const int (&last)[NT], int least, int lane) {
     if (mine >= tiles) return;
     const Loader8<D, kToken> ld(a, s, kvh, lane);
@@ -432,8 +438,8 @@ __device__ __forceinline__ Query8 query8(const CachedArgs& a, int kvh, int x, in
 
 // Writes the output (whole) of the rows x0 + 16 n + c, or their state to split
 // `split` of the workspace.
-template <int D, int NT, bool kToken>
-__device__ __forceinline__ void store8(const CachedArgs& a, const Rows8<D, NT, kToken>& r, const float (&l)[NT], int kvh, int x0,
+template <int D, int NT>
+__device__ __forceinline__ void store8(const CachedArgs& a, const Rows8<D, NT>& r, const float (&l)[NT], int kvh, int x0,
                                        int rows, int split, bool whole, int lane) {
     const int c = lane & 15, g = lane >> 4;
     asm volatile("" : "+s"(x0));                         // worked out here, not kept in registers through the loop
@@ -477,7 +483,7 @@ __device__ __forceinline__ void keys8(const Cached8Args& a, const Keys8& s, int 
         load_query8<D>(q[n], ca.q + y.token * ca.q_stride + y.head * D, lane >> 4, y.exists);
         last[n] = len - ca.L + y.token % ca.L;
     }
-    Rows8<D, NT, kToken> r;
+    Rows8<D, NT> r;
     r.clear();
     walk8<D, NT, kInt8, kToken>(r, q, a, s, kvh, tiles, wave, U, last, len - ca.L, lane);
     float l[NT];
@@ -512,7 +518,7 @@ __device__ __forceinline__ void keys8(const Cached8Args& a, const Keys8& s, int 
             }
         }
     }
-    if (wave == 0) store8<D, NT, kToken>(ca, r, l, kvh, x0, rows, split, whole, lane);
+    if (wave == 0) store8<D, NT>(ca, r, l, kvh, x0, rows, split, whole, lane);
 }
 
 // Prefix keys for many rows: 4 waves of 32 query rows share each tile.  They turn
@@ -542,7 +548,7 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
     const Loader8<D, kToken> ld(a, s, kvh, lane);
     const float cs = ca.scale * kLog2e;
     const int tiles = s.ptiles;
-    Rows8<D, NT, kToken> r;
+    Rows8<D, NT> r;
     r.clear();
     // Wave w brings block w of the keys, and of V channels D / 4 w ..; C times 16 codes a lane of each, 2 C operands.
     constexpr int C = D / 64;
@@ -695,7 +701,7 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
         quarter(IC<1>{});
         quarter(IC<2>{});
         quarter(IC<3>{});
-        sum8<D, NT, kToken>(r, p, f);
+        sum8(r, p, f, lane);
         auto region = [&](auto b_c) {
             constexpr int b = decltype(b_c)::value;
             bf16x8 next[2];
@@ -742,7 +748,7 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
     float l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) l[n] = r.sum(n);
-    store8<D, NT, kToken>(ca, r, l, kvh, x0, rows, split, false, lane);
+    store8<D, NT>(ca, r, l, kvh, x0, rows, split, false, lane);
 }
 
 // Forms of a call (see cached8_plan).
