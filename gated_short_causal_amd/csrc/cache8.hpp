@@ -42,7 +42,7 @@ __device__ __forceinline__ void decode4(uint32_t c, float* f) {
 // Four values, in steps of their scale, as codes: rounded to nearest even,
 // beyond the largest code the largest; a NaN is 0 (int8) or stays NaN (e4m3).
 template <bool kInt8>
-__device__ __forceinline__ uint32_t encode4(const float* f) {
+__device__ __forceinline__ uint32_t encode4_any(const float* f) {
     float x[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -57,6 +57,25 @@ __device__ __forceinline__ uint32_t encode4(const float* f) {
     } else {
         const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(x[0], x[1], 0, false);
         return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(x[2], x[3], lo, true);
+    }
+}
+
+// The same for values that are numbers and whose codes the scale holds (below
+// 127.5, 464): 11 instead of 30 instructions for int8.  x + 1.5 * 2^23 rounds x to a
+// whole number (nearest even) whose low byte is the code; not fused with the product
+// that x came from, which is rounded first.
+template <bool kInt8>
+__device__ __forceinline__ uint32_t encode4(const float* f) {
+#pragma clang fp contract(off)
+    if constexpr (kInt8) {
+        uint32_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = __float_as_uint(f[i] + 12582912.f);
+        const uint32_t lo = __builtin_amdgcn_perm(x[1], x[0], 0x0c0c0400u), hi = __builtin_amdgcn_perm(x[3], x[2], 0x04000c0cu);
+        return lo | hi;
+    } else {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
+        return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], lo, true);
     }
 }
 

@@ -11,6 +11,7 @@
 // fp32 (truncated below 2^-28).
 #include "attn_common.hpp"
 #include "hybrid.hpp"
+#include "seq_find.hpp"
 
 namespace lfm2sc {
 
@@ -32,26 +33,15 @@ __device__ __forceinline__ float2 cos_sin(int position, float freq) {
     return make_float2(n == 1 || n == 2 ? -co : co, n >= 2 ? -si : si);
 }
 
-// The row's position; false: the row belongs to no sequence.  Row offsets are searched for the last sequence that
-// begins at or before the row.
+// The row's position; false: the row belongs to no sequence.
 __device__ __forceinline__ bool row_position(const RotaryRows& a, int64_t row, int& position) {
     if (a.cu == nullptr) {
         position = a.positions[row];
         return true;
     }
-    const int lane = threadIdx.x & 63;
-    int lo = 0, hi = a.N;                        // cu[lo] <= row (or lo == 0), cu[hi] > row (or hi == N)
-    while (hi - lo > 1) {                        // 64 parts a step
-        const int step = (hi - lo + 63) / 64, at = lo + (lane + 1) * step;
-        const int part = __popcll(__ballot(at < hi && a.cu[min(at, a.N)] <= row));
-        const int next = lo + part * step;
-        hi = min(next + step, hi);
-        lo = next;
-    }
-    const int begin = a.cu[lo], end = a.cu[lo + 1];
-    const int64_t at = row - begin;
-    position = (int)at + (a.positions == nullptr ? 0 : a.positions[lo]);
-    return at >= 0 && row < end;
+    const SeqAt s = find_seq(a.cu, a.positions, a.N, [&](int, int at) { return at <= row; });
+    position = (int)(row - s.begin) + s.extra;
+    return row >= s.begin && row < s.end;
 }
 
 // n (<= 8) elements of a row, 16-byte aligned unless kLoose (then aligned to an element only).
