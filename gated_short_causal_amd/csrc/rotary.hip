@@ -81,9 +81,10 @@ __device__ __forceinline__ void store_run(E* p, int n, const Raw8<E>& r) {
     }
 }
 
-// A lane's item is two runs of up to 8 elements of one head.  Half layout: columns c and R / 2 + c of R rotated ones,
-// then the columns from R on; interleaved: 16 neighbouring columns.  kLoose: R / 2 is no multiple of 8 (half layout),
-// so the second run starts at any element and the last ones are short.
+// A lane's item is two runs of up to 8 elements of one head, chosen so that neighbouring lanes' runs are neighbours
+// (a lane with 16 neighbouring elements would use half of each line an access touches).  Half layout: columns c and R / 2 + c
+// of the R rotated ones, then of the columns from R on one of either half; interleaved: a run of either half of the columns.
+// kLoose: R / 2 is no multiple of 8 (half layout), so runs may begin at any element and the last ones are short.
 template <typename E, bool kInterleaved, bool kLoose>
 __global__ __launch_bounds__(64 * kRotW) void rotary_kernel(RotaryArgs<E> a) {
     __shared__ float2 table[kRotW][kRotaryMaxD / 2];
@@ -99,7 +100,7 @@ __global__ __launch_bounds__(64 * kRotW) void rotary_kernel(RotaryArgs<E> a) {
     struct Item {
         const E* src;
         E* dst;
-        int c[2], n[2], pair;        // pair: number of the first rotated pair; -1: columns that stay
+        int c[2], n[2], pair[2];     // pair: number of the first pair, of each run (half layout: of both; -1: columns that stay)
     };
     auto item = [&](int i) {
         Item x;
@@ -108,22 +109,24 @@ __global__ __launch_bounds__(64 * kRotW) void rotary_kernel(RotaryArgs<E> a) {
         x.src = (k ? a.k + row * a.k_stride : a.q + row * a.q_stride) + (int64_t)(k ? head - a.Hq : head) * a.D;
         x.dst = (k ? a.k_out + row * a.k_out_stride : a.q_out + row * a.q_out_stride) + (int64_t)(k ? head - a.Hq : head) * a.D;
         if constexpr (kInterleaved) {
-            x.c[0] = 16 * j;
-            x.c[1] = 16 * j + 8;
+            x.c[0] = 8 * j;
+            x.c[1] = 8 * (j + (int)per_head);
             x.n[0] = 8;
             x.n[1] = x.c[1] < a.D ? 8 : 0;
-            x.pair = 8 * j;
+            x.pair[0] = x.c[0] / 2;
+            x.pair[1] = x.c[1] / 2;
         } else if (j < full + tail) {
             x.c[0] = 8 * j;
             x.c[1] = half + 8 * j;
             x.n[0] = x.n[1] = kLoose ? min(8, half - 8 * j) : 8;
-            x.pair = 8 * j;
+            x.pair[0] = 8 * j;
         } else {
-            x.c[0] = R + 16 * (j - full - tail);
-            x.c[1] = x.c[0] + 8;
+            const int m = j - full - tail;
+            x.c[0] = R + 8 * m;
+            x.c[1] = x.c[0] + 8 * ((int)per_head - full - tail);
             x.n[0] = kLoose ? min(8, a.D - x.c[0]) : 8;
             x.n[1] = max(0, min(8, a.D - x.c[1]));
-            x.pair = -1;
+            x.pair[0] = -1;
         }
         return x;
     };
@@ -158,7 +161,7 @@ __global__ __launch_bounds__(64 * kRotW) void rotary_kernel(RotaryArgs<E> a) {
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        const int at = x[u].pair + 4 * s + p;
+                        const int at = x[u].pair[s] + p;
                         const float2 t = cs[min(at, half - 1)];
                         const float b = f[s][2 * p], c = f[s][2 * p + 1];
                         const bool turns = at < half;
@@ -166,8 +169,8 @@ __global__ __launch_bounds__(64 * kRotW) void rotary_kernel(RotaryArgs<E> a) {
                         f[s][2 * p + 1] = turns ? __builtin_fmaf(c, t.x, b * t.y) : c;
                     }
             } else {
-                const bool turns = x[u].pair >= 0;
-                const int p0 = turns ? x[u].pair : 0;
+                const bool turns = x[u].pair[0] >= 0;
+                const int p0 = turns ? x[u].pair[0] : 0;
 #pragma unroll
                 for (int p = 0; p < 8; ++p) {
                     const float2 t = cs[kLoose ? min(p0 + p, half - 1) : p0 + p];
