@@ -44,55 +44,58 @@ __device__ __forceinline__ bool row_position(const RotaryRows& a, int64_t row, i
     return row >= s.begin && row < s.end;
 }
 
-// n (<= 8) elements of a row, 16-byte aligned unless kLoose (then aligned to an element only).
-template <typename E, bool kLoose>
+// How a layout falls into runs of 8 elements.  kAligned: every run is 16-byte aligned.  The others (half layout, R / 2 no
+// multiple of 8) begin at any element.  kOverlap: the last run of a part begins early enough to be whole, so that some
+// elements are computed and written twice, the same both times; not in place, where they may be rotated already.
+// kShort: it has fewer elements, one access each (32768 rows of 18 heads of 128 with R = 100: 105 us, kOverlap 66).
+enum Runs { kAligned, kOverlap, kShort };
+
+// n elements of a row: 8 or none, or for kShort any number up to 8.
+template <typename E, int kRuns>
 __device__ __forceinline__ Raw8<E> load_run(const E* p, int n) {
-    Raw8<E> r;
-    if constexpr (kLoose) {
-        if (n == 8) {
-            __builtin_memcpy(&r, p, sizeof(r));
-        } else {
-            E e[8] = {};
+    Raw8<E> r{};
+    if (n == 8) {
+        if constexpr (kRuns == kAligned) r = ld8<E>(p);
+        else __builtin_memcpy(&r, p, sizeof(r));
+    } else if constexpr (kRuns == kShort) {
+        E e[8] = {};
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) e[j] = p[j];
-            __builtin_memcpy(&r, e, sizeof(r));
-        }
-    } else {
-        if (n == 8) r = ld8s<E, 1>(p);
-        else r = Raw8<E>{};
+        for (int j = 0; j < 8; ++j)
+            if (j < n) e[j] = p[j];
+        __builtin_memcpy(&r, e, sizeof(r));
     }
     return r;
 }
-template <typename E, bool kLoose>
+template <typename E, int kRuns>
 __device__ __forceinline__ void store_run(E* p, int n, const Raw8<E>& r) {
-    if constexpr (kLoose) {
-        if (n == 8) {
-            __builtin_memcpy(p, &r, sizeof(r));
-        } else {
-            E e[8];
-            __builtin_memcpy(e, &r, sizeof(r));
+    if (n == 8) {
+        if constexpr (kRuns == kAligned) st8s<E, 2>(p, r);
+        else __builtin_memcpy(p, &r, sizeof(r));
+    } else if constexpr (kRuns == kShort) {
+        E e[8];
+        __builtin_memcpy(e, &r, sizeof(r));
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < n) p[j] = e[j];
-        }
-    } else {
-        if (n == 8) st8s<E, 2>(p, r);
+        for (int j = 0; j < 8; ++j)
+            if (j < n) p[j] = e[j];
     }
 }
 
 // A lane's item is two runs of up to 8 elements of one head, chosen so that neighbouring lanes' runs are neighbours
 // (a lane with 16 neighbouring elements would use half of each line an access touches).  Half layout: columns c and R / 2 + c
 // of the R rotated ones, then of the columns from R on one of either half; interleaved: a run of either half of the columns.
-// kLoose: R / 2 is no multiple of 8 (half layout), so runs may begin at any element and the last ones are short.
-template <typename E, bool kInterleaved, bool kLoose>
+//
+// Rows are stored past the caches' reach (nt) and read as usual: read nt too, 8 prompts take 20.3 instead of 16.8 us and
+// 16384 rows 40 instead of 33 us; stored as usual, 65536 rows of 40 heads of 64 gain (144 -> 128 us: a run of R = 64 is half
+// a line), everything else loses (32768 interleaved 50 -> 61 us).  Lanes trading runs so that a store fills its lines
+// cost more than they gained (8 prompts 16.8 -> 27.5 us).
+template <typename E, bool kInterleaved, int kRuns>
 __global__ __launch_bounds__(64 * kRotW) void rotary_kernel(RotaryArgs<E> a) {
     __shared__ float2 table[kRotW][kRotaryMaxD / 2];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const uint32_t unit = blockIdx.x * (uint32_t)kRotW + (uint32_t)wave;       // < 2^26, see the launcher
     const int64_t row = unit / (uint32_t)a.parts;
     if (row >= a.r.T) return;
-    const int R = a.R, half = R / 2, full = half / 8, tail = kLoose ? 1 : 0;
+    const int R = a.R, half = R / 2, full = half / 8, tail = kRuns == kAligned ? 0 : 1;
     const int first = (int)(unit % (uint32_t)a.parts) * a.part_items, last = min(first + a.part_items, a.items);
     const uint32_t per_head = (uint32_t)a.per_head;
     float2* cs = table[wave];
@@ -116,16 +119,20 @@ __global__ __launch_bounds__(64 * kRotW) void rotary_kernel(RotaryArgs<E> a) {
             x.pair[0] = x.c[0] / 2;
             x.pair[1] = x.c[1] / 2;
         } else if (j < full + tail) {
-            x.c[0] = 8 * j;
-            x.c[1] = half + 8 * j;
-            x.n[0] = x.n[1] = kLoose ? min(8, half - 8 * j) : 8;
-            x.pair[0] = 8 * j;
+            x.pair[0] = kRuns == kOverlap ? min(8 * j, half - 8) : 8 * j;
+            x.c[0] = x.pair[0];
+            x.c[1] = half + x.pair[0];
+            x.n[0] = x.n[1] = kRuns == kShort ? min(8, half - 8 * j) : 8;
         } else {
             const int m = j - full - tail;
             x.c[0] = R + 8 * m;
             x.c[1] = x.c[0] + 8 * ((int)per_head - full - tail);
-            x.n[0] = kLoose ? min(8, a.D - x.c[0]) : 8;
-            x.n[1] = max(0, min(8, a.D - x.c[1]));
+            x.n[0] = kRuns == kShort ? min(8, a.D - x.c[0]) : 8;
+            x.n[1] = kRuns == kShort ? max(0, min(8, a.D - x.c[1])) : x.c[1] < a.D ? 8 : 0;
+            if (kRuns == kOverlap) {
+                x.c[0] = min(x.c[0], a.D - 8);
+                x.c[1] = min(x.c[1], a.D - 8);
+            }
             x.pair[0] = -1;
         }
         return x;
@@ -139,7 +146,7 @@ __global__ __launch_bounds__(64 * kRotW) void rotary_kernel(RotaryArgs<E> a) {
         for (int u = 0; u < kRotU; ++u) {
             x[u] = item(min(i0 + u * 64 + lane, last - 1));
 #pragma unroll
-            for (int s = 0; s < 2; ++s) v[u][s] = load_run<E, kLoose>(x[u].src + x[u].c[s], x[u].n[s]);
+            for (int s = 0; s < 2; ++s) v[u][s] = load_run<E, kRuns>(x[u].src + x[u].c[s], x[u].n[s]);
         }
         if (!ready) {                                        // the first loads are under way
             ready = true;
@@ -173,7 +180,7 @@ __global__ __launch_bounds__(64 * kRotW) void rotary_kernel(RotaryArgs<E> a) {
                 const int p0 = turns ? x[u].pair[0] : 0;
 #pragma unroll
                 for (int p = 0; p < 8; ++p) {
-                    const float2 t = cs[kLoose ? min(p0 + p, half - 1) : p0 + p];
+                    const float2 t = cs[kRuns == kShort ? min(p0 + p, half - 1) : p0 + p];
                     const float b = f[0][p], c = f[1][p];
                     f[0][p] = turns ? __builtin_fmaf(b, t.x, -c * t.y) : b;
                     f[1][p] = turns ? __builtin_fmaf(c, t.x, b * t.y) : c;
@@ -181,7 +188,7 @@ __global__ __launch_bounds__(64 * kRotW) void rotary_kernel(RotaryArgs<E> a) {
             }
             if (i0 + u * 64 + lane < last) {
 #pragma unroll
-                for (int s = 0; s < 2; ++s) store_run<E, kLoose>(x[u].dst + x[u].c[s], x[u].n[s], from_f32<E>(f[s]));
+                for (int s = 0; s < 2; ++s) store_run<E, kRuns>(x[u].dst + x[u].c[s], x[u].n[s], from_f32<E>(f[s]));
             }
         }
     }
@@ -190,10 +197,13 @@ __global__ __launch_bounds__(64 * kRotW) void rotary_kernel(RotaryArgs<E> a) {
 template <typename E>
 hipError_t launch_rotary(RotaryArgs<E> a, bool interleaved, hipStream_t s) {
     const int half = a.R / 2;
-    const bool loose = !interleaved && half % 8 != 0;
-    const bool in_place = (const E*)a.q_out == a.q && (a.Hkv == 0 || (const E*)a.k_out == a.k);
-    const int rest = in_place ? 0 : (a.D - a.R + 15) / 16;   // in place, the columns that stay are there
-    a.per_head = interleaved ? ((in_place ? a.R : a.D) + 15) / 16 : half / 8 + (loose ? 1 : 0) + rest;
+    const bool in_place = (const E*)a.q_out == a.q || (a.Hkv > 0 && (const E*)a.k_out == a.k);
+    const bool all_in_place = (const E*)a.q_out == a.q && (a.Hkv == 0 || (const E*)a.k_out == a.k);
+    const int runs = interleaved || half % 8 == 0                                              ? kAligned
+                     : !in_place && half >= 8 && (a.D == a.R || a.D - a.R >= 8) ? kOverlap
+                                                                                : kShort;
+    const int rest = all_in_place ? 0 : (a.D - a.R + 15) / 16;       // in place, the columns that stay are there
+    a.per_head = interleaved ? ((all_in_place ? a.R : a.D) + 15) / 16 : half / 8 + (runs != kAligned ? 1 : 0) + rest;
     a.items = a.per_head * (a.Hq + a.Hkv);
     // few rows: a row's items go to several waves, so that the card has 2048 of them
     const int64_t want = 2048 / a.r.T, most = (a.items + 63) / 64;
@@ -203,9 +213,10 @@ hipError_t launch_rotary(RotaryArgs<E> a, bool interleaved, hipStream_t s) {
     const int64_t blocks = (a.r.T * a.parts + kRotW - 1) / kRotW;
     if (too_many(blocks, 64 * kRotW)) return hipErrorInvalidConfiguration;
     const dim3 grid((uint32_t)blocks), block(64 * kRotW);
-    if (interleaved) hipLaunchKernelGGL((rotary_kernel<E, true, false>), grid, block, 0, s, a);
-    else if (loose) hipLaunchKernelGGL((rotary_kernel<E, false, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((rotary_kernel<E, false, false>), grid, block, 0, s, a);
+    if (interleaved) hipLaunchKernelGGL((rotary_kernel<E, true, kAligned>), grid, block, 0, s, a);
+    else if (runs == kAligned) hipLaunchKernelGGL((rotary_kernel<E, false, kAligned>), grid, block, 0, s, a);
+    else if (runs == kOverlap) hipLaunchKernelGGL((rotary_kernel<E, false, kOverlap>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((rotary_kernel<E, false, kShort>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 template hipError_t launch_rotary<uint16_t>(RotaryArgs<uint16_t>, bool, hipStream_t);
