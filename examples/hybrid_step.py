@@ -1,6 +1,6 @@
 """The hybrid decoder's operators as a program uses them: one training step of a ShortConv layer and an attention layer,
-and one speculative serving step (verify block through both kinds of layer, draft verification, rollback of the conv
-states).  Sizes: hidden 2048, K = 3, 32 query and 8 key/value heads of 64.  Random weights; `python examples/hybrid_step.py`
+one speculative serving step (verify block through both kinds of layer, draft verification, rollback of the conv
+states), and decoding over a cache of 8-bit codes.  Sizes: hidden 2048, K = 3, 32 query and 8 key/value heads of 64.  Random weights; `python examples/hybrid_step.py`
 on an MI355X.
 """
 import os
@@ -35,8 +35,11 @@ def train_step(lens, dev):
     k, v = kv.split(KV * D, 1)
     dk, dv = d_kv.split(KV * D, 1)
     ws = torch.empty(g.lfm2sc_attn_backward_workspace_bytes(BF, D, HEADS, KV, T, N), dtype=torch.uint8, device=dev)
+    freqs = g.lfm2sc_rotary_freqs(D, base=1e6).to(dev)
+    g.lfm2sc_rotary(q, q, D, freqs, cu_seqlens=cu, k=k, k_out=k)
     g.lfm2sc_attn_prefill(q, k, v, cu, D, out, lse=lse)
     g.lfm2sc_attn_backward(q, k, v, cu, D, out, lse, do, dq, dk, dv, ws)
+    g.lfm2sc_rotary(dq, dq, D, freqs, cu_seqlens=cu, k=dk, k_out=dk, inverse=True)
     return {"y": y, "d_conv": d_conv, "dw": dw, "out": out, "lse": lse, "dq": dq, "d_kv": d_kv}
 
 
@@ -74,6 +77,44 @@ def speculative_step(seqs, drafts, prefix, dev, vocab=4096, page=16):
     return {"y": y, "out": out, "accepted": accepted, "next": following, "pool": pool, "tape": tape, "slots": slots}
 
 
+def decode_8bit(prompts, steps, prefix, dev, page=64, block=16, codes=torch.float8_e4m3fn):
+    """Attention layer of `steps` decode steps over a cache of 8-bit codes: a shared prefix and prompts of their own are
+    written once, then each step rotates, writes and attends one token per sequence; returns the steps' outputs."""
+    N, limit = len(prompts), max(prompts) + steps
+    most, shared = -(-limit // page), -(-prefix // page)
+    P = shared + N * most
+    k_pages, v_pages = (torch.empty(P, KV, *shape, dtype=codes, device=dev) for shape in ((page, D), (page // 16, D, 16)))
+    k_scales, v_scales = (torch.empty(P, KV, page // block, device=dev) for _ in range(2))
+    cache = (k_pages, v_pages, k_scales, v_scales)
+    pages = torch.randperm(P, device=dev).to(I32)
+    prefix_pages, table = pages[:shared].contiguous(), pages[shared:].reshape(N, most).contiguous()
+    freqs = g.lfm2sc_rotary_freqs(D, base=1e6).to(dev)
+
+    def rotated(rows, **where):
+        q, k, v = rows.split([HEADS * D, KV * D, KV * D], 1)             # one projection's columns, rotated in place
+        g.lfm2sc_rotary(q, q, D, freqs, k=k, k_out=k, **where)
+        return q, k, v
+
+    width = (HEADS + 2 * KV) * D
+    zero, one = torch.tensor([0, prefix], dtype=I32, device=dev), torch.tensor([prefix], dtype=I32, device=dev)
+    _, k, v = rotated(rand(prefix, width, dev=dev), cu_seqlens=zero)
+    g.lfm2sc_cache8_write(k, v, *cache, prefix_pages[None], one)
+    lens = torch.tensor(prompts, dtype=I32, device=dev)
+    cu = torch.tensor([0] + prompts).cumsum(0).to(I32).to(dev)
+    _, k, v = rotated(rand(sum(prompts), width, dev=dev), cu_seqlens=cu, positions=torch.full((N,), prefix, dtype=I32, device=dev))
+    g.lfm2sc_cache8_write(k, v, *cache, table, lens, cu_seqlens=cu)
+
+    ws = torch.empty(g.lfm2sc_attn_cached8_workspace_bytes(BF, D, HEADS, KV, N, 1, prefix, limit), dtype=torch.uint8, device=dev)
+    outs = []
+    for _ in range(steps):
+        q, k, v = rotated(rand(N, width, dev=dev), positions=lens + prefix)
+        lens += 1
+        g.lfm2sc_cache8_write(k, v, *cache, table, lens)
+        outs.append(torch.empty(N, HEADS * D, dtype=BF, device=dev))
+        g.lfm2sc_attn_cached8(q, *cache, prefix_pages, prefix, table, lens, 1, outs[-1], ws, max_suffix_len=limit)
+    return {"out": torch.stack(outs), "lens": lens, "cache": cache, "table": table, "prefix_pages": prefix_pages}
+
+
 if __name__ == "__main__":
     device = torch.device("cuda:0")
     grads = train_step([700, 1, 323], device)
@@ -81,3 +122,5 @@ if __name__ == "__main__":
     step = speculative_step(16, 7, 1000, device)
     torch.cuda.synchronize()
     print("speculative step: accepted", step["accepted"].tolist(), "next", step["next"].tolist())
+    decoded = decode_8bit([100, 7, 333], 4, 500, device)
+    print("8-bit decoding:", tuple(decoded["out"].shape), "lengths", decoded["lens"].tolist())

@@ -103,6 +103,7 @@ size_t cached_bytes(int D, int Hq, int Hkv, int N, int L, int prefix_len, int ma
 
 size_t cached8_bytes(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_suffix) {
     const Cached8Plan p = cached8_plan(D, Hq, Hkv, N, L, prefix_len, max_suffix);
+    if (p.prefix_splits + p.suffix_splits <= 1) return 0;  // nothing to join: the rows go straight to `out`
     const size_t rows = (size_t)N * (size_t)L * (size_t)Hq * (size_t)(p.prefix_splits + p.suffix_splits);
     return round_up(rows * (size_t)D * 4) + round_up(rows * 8);
 }

@@ -249,6 +249,8 @@ def lfm2sc_rotary(q, q_out, D, freqs, positions=None, cu_seqlens=None, k=None, k
             raise ValueError("cu_seqlens must be a 1-D int32 tensor of N+1 row offsets")
         N = cu_seqlens.numel() - 1
         cu, pos = _vec(cu_seqlens, "cu_seqlens", dev, _I32, 1), _vec(positions, "positions", dev, _I32, N)
+        if pos is not None and positions.numel() != N:
+            raise ValueError(f"with cu_seqlens, positions are those of the {N} sequences' first rows, got {positions.numel()}")
     rc = _lib.hybrid_lib().lfm2sc_rotary(
         code, D, 2 * freqs.numel(), int(interleaved), int(inverse), q.data_ptr(), qs, q_out.data_ptr(), qos, Hq, kp, ks, kop, kos,
         Hkv, T, pos, cu, N, _vec(freqs, "freqs", dev, _F32, 1), magnitude, binding._stream(q.device))

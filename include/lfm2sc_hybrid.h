@@ -183,8 +183,8 @@ int lfm2sc_accept_drafts(int dtype, int V, int num_seqs, int L,
                          void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
- * Rotary positions.  Passage: MAX LFM2 attention layers (A22 of the hybrid
- * decoders' draft models: both pairings); the rotation is the published one.
+ * Rotary positions: the rotation of the published method, for the attention layers
+ * and for draft models, which pair channels either way.
  */
 
 /* Frequencies for longer contexts than the model was trained on. */
@@ -304,7 +304,7 @@ int lfm2sc_cache8_read(int dtype, int format, int D, int num_kv_heads,
 
 /*
  * Bytes of workspace lfm2sc_attn_cached8 needs; 0 for invalid sizes, when num_seqs or L
- * is 0, and for few keys, which need none.
+ * is 0, and for calls that need none (few keys; many rows without a prefix).
  */
 size_t lfm2sc_attn_cached8_workspace_bytes(int dtype, int D, int num_heads, int num_kv_heads, int num_seqs, int L,
                                            int prefix_len, int max_suffix_len);

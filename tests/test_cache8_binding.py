@@ -41,7 +41,7 @@ def test_rotary_marshals(lib):
     (dict(k_out=None), ValueError), (dict(k=None), ValueError), (dict(k=torch.zeros(10, 128)), TypeError), (dict(positions=None), ValueError),
     (dict(positions=torch.zeros(9, dtype=I32)), ValueError), (dict(positions=torch.zeros(10, dtype=torch.int64)), TypeError),
     (dict(freqs=torch.zeros(16).double()), TypeError), (dict(freqs=torch.zeros(32)[::2]), ValueError), (dict(freqs=torch.zeros(0)), ValueError),
-    (dict(cu_seqlens=torch.zeros(12, dtype=I32)), ValueError), (dict(cu_seqlens=torch.zeros(2, 2, dtype=I32)), ValueError), (dict(D=0), ValueError),
+    (dict(cu_seqlens=torch.zeros(12, dtype=I32)), ValueError), (dict(cu_seqlens=torch.zeros(3, dtype=I32)), ValueError), (dict(cu_seqlens=torch.zeros(2, 2, dtype=I32)), ValueError), (dict(D=0), ValueError),
     (dict(q=torch.zeros(10, 256, dtype=torch.float16)), TypeError), (dict(q=torch.zeros(10, 512, dtype=BF)[:, ::2]), ValueError),
 ])
 def test_rotary_refuses(lib, change, err):

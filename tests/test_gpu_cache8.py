@@ -1,9 +1,11 @@
 """The 8-bit cache on the GPU: codes and scales against the oracle bit for bit, values read back bit for bit, and attention
 over it against fp64.
 
-Tolerance of the attention: the probability times the value's scale is rounded to bf16 once, the output once: HALF * (sum p |v|
-+ |out|); fp32 scores: D products summed in fp32 and two more roundings move a score, hence a probability relatively, by
-(D + 10) 2^-24 of the score's terms.
+Tolerance of the attention: out = sum w v' / sum w / vs with w = p vs rounded to bf16 (v' the code, vs its scale), so a row's
+probabilities p are p (1 + d), |d| <= HALF, above and below: sum p d (v - out) <= HALF (sum p |v| + |out|), and the output's own
+rounding HALF |out| more.  1 / vs is held as two bf16 numbers, 2^-16 off; that and products of errors are the factor 1 + 2^-7.
+fp32: D products summed and a few more roundings of a score move it by at most (D + 10) 2^-24 of its terms' magnitudes, hence a
+probability relatively by as much (D is at most 128), again above and below: twice that of sum p |v|, as |out| is below it.
 """
 import numpy as np
 import pytest
@@ -236,7 +238,7 @@ def _attend(c, q, prefix_pages, prefix, table, lens, L, out_pad=8, **kw):
 def _close(got, want, what=""):
     out, spread, most = want
     D = 128
-    tol = HALF * (spread + np.abs(out)) * (1 + 2.0 ** -7) + (D + 10) * 2.0 ** -23 * (1 + most) * spread + 1e-30
+    tol = HALF * (spread + 2 * np.abs(out)) * (1 + 2.0 ** -7) + (D + 10) * 2.0 ** -23 * (1 + most) * spread + 1e-30
     got = got.detach().cpu().double().numpy()
     bad = ~(np.abs(got - out) <= tol)
     assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} out of tolerance, first at {np.argwhere(bad)[0]}: {got[bad][0]} for "
