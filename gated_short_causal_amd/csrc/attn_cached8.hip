@@ -15,9 +15,16 @@ Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, i
     p.prefix_splits = 0;
     p.prefix_chunk = 0;
     p.prefix_blocks = 0;
-    p.form = base <= 512 && ptiles + otiles <= (base >= 128 ? 32 : 16) ? kDirect8
-             : prefix_len > 0 && rows > kSharedRows                              ? kShared8
-                                                                        : kSplit8;
+    // Direct: no workspace, no join, but every sequence reads the prefix itself and a workgroup walks all of its keys.  Direct
+    // and split, 8 heads of 64, keys behind no prefix: 1 x 1000 6.3 and 6.9 us, 1 x 2000 8.5 and 7.1; 16 x 2000 9.7 and
+    // 11.3; 32 x 4000 17.6 and 19.3; 64 x 4000 30.6 and 29.7; 128 x 2000 28.3 and 31.5; 256 x 2000 equal; 8 x 8000 23.9 and 16.7.
+    // Rows in blocks of 32 (8 tokens of 5 heads of 128): 16 x 4000 34.6 and 41.7, 64 x 999 52 and 36.  Behind a prefix (32
+    // sequences, 4096 + 600): 15.9 and 12.1.
+    const int64_t few = base < 128 ? 16 : base < 256 || base > 512 || ptiles > 0 ? 32 : 64;
+    // Shared: 128 query rows a workgroup.  Shared and split, rows behind 4096 + 600 keys: 64 rows 12.2 and 9.5 us, 256 rows 17.7
+    // and 17.3, 1024 rows 33 and 38; behind 16384 + 100: 128 rows 24.4 and 22.5, 160 rows 26.5 and 27.5, 256 rows 29 and 37.
+    if (base <= (ptiles > 0 || rows_unit == 32 ? 512 : 1024) && ptiles + otiles <= few) p.form = kDirect8;
+    else p.form = prefix_len > 0 && rows > kSharedRows ? kShared8 : kSplit8;
     if (p.form == kDirect8) {
         p.suffix_splits = 0;
         p.suffix_blocks = base;
@@ -25,7 +32,9 @@ Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, i
     }
     if (prefix_len > 0) {
         const int64_t rows_wg = p.form == kShared8 ? kSharedRows : rows_unit, row_blocks = (rows + rows_wg - 1) / rows_wg;
-        // seconds at 8e14 flops/s and 5e12 bytes/s; a batch fills about half of its longest suffix
+        // The prefix gets the workgroups that the card holds, or where the suffixes take long the share that its products take
+        // of both (1024 rows behind 4096 + 600: 33 us, with all of them 44).  Seconds at 8e14 flops/s and 5e12 bytes/s; a
+        // batch fills about half of its longest suffix.
         const double product = 4. * rows * Hkv * D * prefix_len / 8e14, read = (double)N * max_suffix * Hkv * D / 5e12;
         const double share = product / (product + read);
         const double slots = p.form == kShared8 ? 256. * form_per_simd(D, 1, kShared8) * (share > 0.8 ? 1. : share) : 256.;
@@ -36,7 +45,10 @@ Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, i
         p.prefix_splits = (int)((ptiles + per - 1) / per);
         p.prefix_blocks = row_blocks * Hkv * p.prefix_splits;
     }
-    const int64_t most = (otiles + 3) / 4, want = std::min<int64_t>((rows_unit == 16 ? 2048 : 1024) / base, 32);
+    // Suffixes are split, down to 4 tiles, up to 2048 units of a workgroup; of 32 rows up to 1024 (64 x 8 tokens, 999 keys, no
+    // prefix: 36 us, with 2048 53), of the shared form, a wave each, up to 4096 (1024 rows behind 4096 + 2000: 75 us, with 2048 80).
+    const int64_t units = rows_unit == 32 ? 1024 : p.form == kShared8 ? 4096 : 2048;
+    const int64_t most = (otiles + 3) / 4, want = std::min<int64_t>(units / base, 32);
     p.suffix_splits = (int)(want < 1 ? 1 : want < most ? want : most);
     if (p.suffix_splits < 1) p.suffix_splits = 1;
     const int per_wg = form_waves(p.form) / own_waves(p.form);
