@@ -21,12 +21,11 @@
 // Nothing but the waves' join goes through LDS.
 //
 // Measured (one MI355X, device time): 64 sequences of up to 16384 keys, 24/8 heads of
-// 128, a scale a token 213 us (543 MB, 2.5 TB/s of codes at half-full ragged lengths;
-// 1 GiB copies reach 5.1): reads bound it, 1.5 of 2 waves a SIMD busy on average, since
-// the longest sequence ends last.  256 sequences of up to 600 (2000) keys behind no
-// prefix, 32/8 heads of 64: 19.4 (61) us for 17 (51) at the copy's rate.  One user, 500 +
-// 37 keys: 5.2 us, a chain of four dependent reads.  Three waves a SIMD for D = 128, with
-// the registers that leaves, took 262 us instead of 217 (64 x 16384).
+// 128, a scale a token: 212 us for 1.13 GB, 5.3 TB/s (1 GiB copies reach 5.1): reads
+// bound it.  256 sequences of up to 600 (2000) keys behind no prefix, 32/8 heads of 64:
+// 19.4 (61) us for 17 (51) at the copy's rate.  One user, 500 + 37 keys: 5.2 us, a chain
+// of four dependent reads.  Three waves a SIMD for D = 128, with the registers that
+// leaves, took 262 us instead of 217 (64 x 16384).
 #pragma once
 
 #include "attn_common.hpp"
