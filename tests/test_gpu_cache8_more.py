@@ -292,3 +292,53 @@ def test_example_decodes():
     for codes in (torch.float8_e4m3fn, torch.int8):
         r = hybrid_step.decode_8bit([20, 3], 3, 70, torch.device(DEV), codes=codes)
         assert r["out"].shape == (3, 2, 2048) and torch.isfinite(r["out"].float()).all() and r["lens"].tolist() == [23, 6]
+
+
+@pytest.mark.parametrize("L", [1, 5, 16, 33])
+@pytest.mark.parametrize("fmt,S,B", [("e4m3", 16, 16), ("int8", 64, 64), ("int8", 32, 1)])
+def test_a_padded_batch(fmt, S, B, L):
+    """Rows of every sequence, of which some hold fewer tokens than rows, or none: the rows before token 0 are left out, written
+    and read."""
+    H, D, lens = 2, 64, [0, 1, L, max(L - 2, 0), 3 * L + 7, 0]
+    N, most = len(lens), -(-(3 * L + 7) // S)
+    c = Cache(fmt, N * most, H, S, D, B, seed=L)
+    table = _table(N, most, N * most)
+    _write(c, _kv(N * L, H, D, BF, 3), table, lens, [L] * N, uniform=True)
+    c.check()
+    out = torch.full((N * L, 2 * H * D), float("nan"), dtype=F32, device=DEV)
+    g.lfm2sc_cache8_read(*c.args, torch.from_numpy(table).to(DEV), torch.tensor(lens, dtype=I32, device=DEV), out[:, :H * D], out[:, H * D:])
+    got = out.cpu().double().numpy().reshape(N, L, 2, H, D)
+    for i, n in enumerate(lens):
+        there = min(n, L)
+        assert np.isnan(got[i, :L - there]).all(), i
+        if there:
+            k, v = o8.values(c.host, table[i], n)
+            want = np.stack([k, v], 1)[n - there:].astype(np.float32)
+            assert (got[i, L - there:] == want).all(), i
+
+
+@pytest.mark.parametrize("N,L,G,prefix,own", [(1, 8, 32, 3000, 20), (1, 1, 64, 0, 700), (2, 70, 2, 900, 100), (3, 5, 16, 40, 9),
+                                              (1, 1, 16, 5000, 0), (1, 200, 1, 64, 200), (40, 1, 64, 0, 300)])
+@pytest.mark.parametrize("fmt,B", [("int8", 16), ("e4m3", 1)])
+def test_wide_groups_and_long_blocks(N, L, G, prefix, own, fmt, B):
+    """One key/value head for many query heads, blocks of more rows than a tile has, and a prefix with nothing behind it."""
+    Hkv, D, S = 1, 64, 32
+    most, npre = -(-max(own, 1) // S), -(-prefix // S)
+    P = npre + N * most
+    c = Cache(fmt, P, Hkv, S, D, B, seed=G)
+    order = np.random.default_rng(1).permutation(P).astype(np.int32)
+    pp, table, lens = order[:npre], order[npre:].reshape(N, most), [max(own - 3 * i, 0) for i in range(N)]
+    q = torch.randn(N * L, Hkv * G * D, generator=torch.Generator().manual_seed(1)).to(BF)
+    got = _attend(c, q, pp if npre else None, prefix, table, lens, L)
+    _close(got, o8.attention(q, c.host, pp if npre else None, prefix, table, lens, L, D ** -0.5))
+
+
+def test_page_numbers_used_by_two_sequences():
+    """Sequences may read the same pages."""
+    c = Cache("int8", 6, 2, 16, 64, 16)
+    table, lens = np.array([[0, 1, 2], [0, 1, 3], [0, 1, 2]], dtype=np.int32), [40, 45, 40]
+    q = torch.randn(3, 256, generator=torch.Generator().manual_seed(1)).to(BF)
+    q[2] = q[0]
+    got = _attend(c, q, None, 0, table, lens, 1)
+    _close(got, o8.attention(q, c.host, None, 0, table, lens, 1, 64 ** -0.5))
+    assert torch.equal(got[0], got[2])

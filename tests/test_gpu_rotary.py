@@ -187,3 +187,15 @@ def test_graph_replays_and_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_positions_at_the_ends_of_their_type(interleaved):
+    """Negative positions turn the other way."""
+    D, H = 64, 3
+    pos = torch.tensor([-2 ** 31, -1, 0, 1, 2 ** 31 - 1], dtype=torch.int32)
+    x = torch.randn(5, H * D, generator=torch.Generator().manual_seed(1))
+    freqs = g.lfm2sc_rotary_freqs(D)
+    y = torch.empty_like(x, device="cuda")
+    g.lfm2sc_rotary(x.cuda(), y, D, freqs.cuda(), positions=pos.cuda(), interleaved=interleaved)
+    _check(y, x, D, freqs, pos.numpy(), interleaved=interleaved)
