@@ -188,8 +188,11 @@ struct Rows8 {
 };
 
 // Scales as the kernels take them.  A scale below 2^-100 (0: a block of zeros)
-// counts as 2^-100, so that its logarithm and reciprocal exist; a NaN stays.
-__device__ __forceinline__ float usable(float scale) { return scale < kMinScale ? kMinScale : scale; }
+// counts as 2^-100, so that its logarithm and reciprocal exist, and its product with
+// the scale of scores as at least 2^-126, as 0 times a masked score of -inf would be a
+// NaN; a NaN stays.
+__device__ __forceinline__ float at_least(float least, float x) { return x < least ? least : x; }
+__device__ __forceinline__ float usable(float scale) { return at_least(kMinScale, scale); }
 
 // Few tiles are masked: what only they need is a branch of its own, not selects in
 // every tile (30 instructions of each row tile's 150).
@@ -219,7 +222,7 @@ struct Scales8 {
     uint32_t one;                // and two values of the operand of l
     __device__ __forceinline__ void set(float ks, float vs, float cs, bool masked, int end, int lane) {
         if (masked) drop_scales<kToken>(ks, vs, end, lane);
-        k = usable(ks) * cs;
+        k = at_least(__FLT_MIN__, usable(ks) * cs);
         v = usable(vs);
         if constexpr (!kToken) {
             log_v = __builtin_amdgcn_logf(v);

@@ -342,3 +342,20 @@ def test_page_numbers_used_by_two_sequences():
     got = _attend(c, q, None, 0, table, lens, 1)
     _close(got, o8.attention(q, c.host, None, 0, table, lens, 1, 64 ** -0.5))
     assert torch.equal(got[0], got[2])
+
+
+@pytest.mark.parametrize("N,L,prefix,own", [(3, 2, 0, 21), (2, 3, 1500, 37), (70, 2, 100, 21)])
+@pytest.mark.parametrize("B", [1, 16])
+def test_a_tiny_scale(N, L, prefix, own, B):
+    """Scores that underflow, of blocks of zeros among them, weigh alike, and keys past the end nothing: every form."""
+    Hkv, G, D, S = 2, 2, 64, 32
+    most, npre = -(-own // S), -(-prefix // S)
+    P = npre + N * most
+    c = Cache("int8", P, Hkv, S, D, B, seed=N)
+    c.args[2][::2] = 0.
+    c.host = c.read()
+    pp, table = np.arange(npre, dtype=np.int32), np.arange(npre, P, dtype=np.int32).reshape(N, most)
+    q = torch.randn(N * L, Hkv * G * D, generator=torch.Generator().manual_seed(1)).to(BF)
+    for scale in (1e-12, 1e-38):
+        got = _attend(c, q, pp if npre else None, prefix, table, [own] * N, L, scale=scale)
+        _close(got, o8.attention(q, c.host, pp if npre else None, prefix, table, [own] * N, L, scale))
