@@ -360,8 +360,22 @@ __global__ __launch_bounds__(64 * kDirectW) void attn_cached_direct_kernel(Cache
     own_part<D, kDirectW, KT, true>(a, buf0, buf1, ml, blockIdx.x, wave, threadIdx.x & 63);
 }
 
+// A value of the lane's row of 16 combined over the row, in the order of a butterfly of distances 1, 2, 4, 8.
+template <typename F>
+__device__ __forceinline__ float over_row(float x, F f) {
+    auto other = [&](auto c) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(c)::value, 0xf, 0xf, false));
+    };
+    x = f(x, other(std::integral_constant<int, 0xb1>{}));      // quad_perm 1 0 3 2
+    x = f(x, other(std::integral_constant<int, 0x4e>{}));      // quad_perm 2 3 0 1
+    x = f(x, other(std::integral_constant<int, 0x141>{}));     // half mirror: a quad's lanes are alike by now
+    return f(x, other(std::integral_constant<int, 0x140>{}));  // mirror
+}
+
 // Joins the splits: a wave per (token row, head).  First every lane takes a
-// split's m and l, then D / 4 lanes times 256 / D groups of them add up o.
+// split's m and l, then D / 4 lanes times 256 / D groups of them add up o.  Up to 16
+// splits: the parts of o are asked for first, and every row of 16 lanes reduces m and
+// l for itself, to the same bits (20480 rows of 128, 4 splits: 12.3 -> 10.1 us, 4.7 TB/s).
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(CachedArgs a) {
     constexpr int kLanes = D / 4, kGroups = 64 / kLanes;
@@ -372,7 +386,34 @@ __global__ __launch_bounds__(256) void attn_join_kernel(CachedArgs a) {
     const int splits = a.prefix_splits + a.suffix_splits;
     float m = kNegInf, l = 0.f;
     float o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int s0 = 0; s0 < splits; s0 += 64) {
+    constexpr int kFew = 16;
+    if (splits <= kFew) {
+        float4 x[kFew / kGroups];
+        float2 ml = make_float2(kNegInf, 0.f);
+        const int mine = lane % kFew;
+        if (mine < splits) ml = *reinterpret_cast<const float2*>(a.part_ml + (mine * rows + row) * 2);
+#pragma unroll
+        for (int u = 0; u < kFew / kGroups; ++u) {
+            const int s = u * kGroups + g;
+            if (u * kGroups >= splits) break;
+            x[u] = *reinterpret_cast<const float4*>(a.part_o + (min(s, splits - 1) * rows + row) * D + 4 * j);
+        }
+        m = over_row(ml.x, [](float x, float y) { return fmaxf(x, y); });
+        const float f = exp2_fast(ml.x - (m == kNegInf ? 0.f : m));
+        l = over_row(f * ml.y, [](float x, float y) { return x + y; });
+#pragma unroll
+        for (int u = 0; u < kFew / kGroups; ++u) {
+            const int s = u * kGroups + g;
+            if (u * kGroups >= splits) break;
+            const float w = __shfl(f, s, 64);
+            if (s < splits) {
+                o[0] = __builtin_fmaf(w, x[u].x, o[0]);
+                o[1] = __builtin_fmaf(w, x[u].y, o[1]);
+                o[2] = __builtin_fmaf(w, x[u].z, o[2]);
+                o[3] = __builtin_fmaf(w, x[u].w, o[3]);
+            }
+        }
+    } else for (int s0 = 0; s0 < splits; s0 += 64) {
         float2 ml = make_float2(kNegInf, 0.f);
         if (s0 + lane < splits) ml = *reinterpret_cast<const float2*>(a.part_ml + ((s0 + lane) * rows + row) * 2);
         float mn = ml.x;

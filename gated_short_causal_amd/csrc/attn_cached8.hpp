@@ -540,8 +540,8 @@ __device__ __forceinline__ void keys8(const Cached8Args& a, const Keys8& s, int 
 // i + 2 and of V in tile i + 1 are staged while p V is added up.
 //
 // 64 x 8 rows of 5 heads of 128 behind 16384 keys (a whole library product of that many
-// flops: 131 us): 196 us with the join (12 us), 187 for e4m3; with suffixes of up to 999
-// keys 211 and 200.  A tile takes two waves of a SIMD 2000 cycles each: 1090 of matrix
+// flops: 131 us): 194 us with the join (10 us), 185 for e4m3; with suffixes of up to 999
+// keys 210 and 196.  A tile takes two waves of a SIMD 2000 cycles each: 1090 of matrix
 // and 1540 of vector instructions, which overlap in part.  Left out one at a time: code
 // conversion -27 us, loads -22, half of p V -21, exponentials -8, reads of LDS -1 to -4;
 // zeros for data -18 (power).  Not kept: 32 x 32 x 16 products (218 us with suffixes: their
