@@ -32,12 +32,16 @@ Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, i
     }
     if (prefix_len > 0) {
         const int64_t rows_wg = p.form == kShared8 ? kSharedRows : rows_unit, row_blocks = (rows + rows_wg - 1) / rows_wg;
-        // The prefix gets the workgroups that the card holds, or where the suffixes take long the share that its products take
-        // of both (1024 rows behind 4096 + 600: 33 us, with all of them 44).  Seconds at 8e14 flops/s and 5e12 bytes/s; a
-        // batch fills about half of its longest suffix.
+        // The prefix of the shared form gets one workgroup a CU, two or as many as the card holds, by the share that its products
+        // take of the time (seconds at 8e14 flops/s and 5e12 bytes/s; a batch fills about half of its longest suffix): numbers
+        // in between wait for the CUs that have one more.  256 and 512 workgroups, us: 32 x 4 rows of 5 heads of 128, 4096 + 999
+        // (share .67) 32.6 and 40.2; 64 x 8, 2048 + 999 (.67) 69.7 and 76.3; 1024 rows of 64, 8192 + 600 (.58) 51.8 and 48.7;
+        // 16384 + 600 (.73) 90.7 and 67.7.  2048 rows, 2048 + 600 (.25): 256 56 us, 128 65; 1024 rows, 4096 + 600 (.4): 256
+        // 34, 192 39, 320 38.
         const double product = 4. * rows * Hkv * D * prefix_len / 8e14, read = (double)N * max_suffix * Hkv * D / 5e12;
         const double share = product / (product + read);
-        const double slots = p.form == kShared8 ? 256. * form_per_simd(D, 1, kShared8) * (share > 0.8 ? 1. : share) : 256.;
+        const int per_cu = p.form == kSplit8 ? 1 : share > 0.8 ? form_per_simd(D, 1, kShared8) : share > (rows_unit == 32 ? 0.7 : 0.55) ? 2 : 1;
+        const double slots = 256. * per_cu;
         const int64_t want = (int64_t)(slots / (double)(row_blocks * Hkv)), most = (ptiles + 3) / 4;
         const int64_t splits = want < 1 ? 1 : want < most ? want : most;
         const int64_t per = (ptiles + splits - 1) / splits;
