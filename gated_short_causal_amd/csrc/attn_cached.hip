@@ -360,16 +360,11 @@ __global__ __launch_bounds__(64 * kDirectW) void attn_cached_direct_kernel(Cache
     own_part<D, kDirectW, KT, true>(a, buf0, buf1, ml, blockIdx.x, wave, threadIdx.x & 63);
 }
 
-// A value of the lane's row of 16 combined over the row, in the order of a butterfly of distances 1, 2, 4, 8.
-template <typename F>
-__device__ __forceinline__ float over_row(float x, F f) {
-    auto other = [&](auto c) {
-        return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), decltype(c)::value, 0xf, 0xf, false));
-    };
-    x = f(x, other(std::integral_constant<int, 0xb1>{}));      // quad_perm 1 0 3 2
-    x = f(x, other(std::integral_constant<int, 0x4e>{}));      // quad_perm 2 3 0 1
-    x = f(x, other(std::integral_constant<int, 0x141>{}));     // half mirror: a quad's lanes are alike by now
-    return f(x, other(std::integral_constant<int, 0x140>{}));  // mirror
+// The value of the lane with another number in bit `d` (1, 2 or 8) of its own.
+template <int d>
+__device__ __forceinline__ float across(float x) {
+    constexpr int kPerm = d == 1 ? 0xb1 : d == 2 ? 0x4e : 0x128;     // quad_perm 1 0 3 2, quad_perm 2 3 0 1, row_ror 8
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), kPerm, 0xf, 0xf, false));
 }
 
 // Joins the splits: a wave per (token row, head).  First every lane takes a
@@ -398,9 +393,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(CachedArgs a) {
             if (u * kGroups >= splits) break;
             x[u] = *reinterpret_cast<const float4*>(a.part_o + (min(s, splits - 1) * rows + row) * D + 4 * j);
         }
-        m = over_row(ml.x, [](float x, float y) { return fmaxf(x, y); });
+        m = fmaxf(ml.x, across<1>(ml.x));
+        m = fmaxf(m, across<2>(m));
+        m = fmaxf(m, __shfl_xor(m, 4, 64));
+        m = fmaxf(m, across<8>(m));
         const float f = exp2_fast(ml.x - (m == kNegInf ? 0.f : m));
-        l = over_row(f * ml.y, [](float x, float y) { return x + y; });
+        l = __builtin_fmaf(f, ml.y, across<1>(f * ml.y));    // as the compiler joins product and sum below
+        l += across<2>(l);
+        l += __shfl_xor(l, 4, 64);
+        l += across<8>(l);
 #pragma unroll
         for (int u = 0; u < kFew / kGroups; ++u) {
             const int s = u * kGroups + g;
