@@ -44,7 +44,7 @@ __device__ __forceinline__ bool row_position(const RotaryRows& a, int64_t row, i
         return true;
     }
     const SeqAt s = find_seq(a.cu, a.positions, a.N, [&](int, int at) { return at <= row; });
-    position = (int)(row - s.begin) + s.extra;
+    position = (int)(row - max(s.begin, 0)) + s.extra;       // offsets count as clamped to [0, T]
     return row >= s.begin && row < s.end;
 }
 

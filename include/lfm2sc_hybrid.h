@@ -224,9 +224,10 @@ int lfm2sc_rotary_freqs(int rotary_dim, double base, int scaling, double factor,
  * k, k_out     the same with num_kv_heads heads; with num_kv_heads 0 they are not
  *              used.
  * positions    int32.  cu_seqlens NULL: [total_T], the rows' positions.  Otherwise
- *              rows are packed sequences (offsets as for lfm2sc_prefill_ragged), row
- *              t of sequence i has position positions[i] + t - cu[i]; positions is
- *              [num_seqs], or NULL for 0.  Rows of no sequence are not written.
+ *              rows are packed sequences (offsets as for lfm2sc_prefill_ragged,
+ *              clamped to [0, total_T]), row t of sequence i has position
+ *              positions[i] + t - cu[i]; positions is [num_seqs], or NULL for 0.
+ *              Rows of no sequence are not written.
  * freqs        [R / 2] fp32, device memory.
  */
 int lfm2sc_rotary(int dtype, int D, int rotary_dim, int interleaved, int inverse,
