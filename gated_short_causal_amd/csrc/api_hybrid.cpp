@@ -101,10 +101,9 @@ size_t cached_bytes(int D, int Hq, int Hkv, int N, int L, int prefix_len, int ma
     return round_up(rows * (size_t)D * 4) + round_up(rows * 8);
 }
 
+// Never less for larger sizes.
 size_t cached8_bytes(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_suffix) {
-    const Cached8Plan p = cached8_plan(D, Hq, Hkv, N, L, prefix_len, max_suffix);
-    if (p.prefix_splits + p.suffix_splits <= 1) return 0;  // nothing to join: the rows go straight to `out`
-    const size_t rows = (size_t)N * (size_t)L * (size_t)Hq * (size_t)(p.prefix_splits + p.suffix_splits);
+    const size_t rows = (size_t)cached8_part_rows(D, Hq, Hkv, N, L, prefix_len, max_suffix);
     return round_up(rows * (size_t)D * 4) + round_up(rows * 8);
 }
 
@@ -584,7 +583,9 @@ int lfm2sc_attn_cached8(int dtype, int format, int D, int num_heads, int num_kv_
     if (max_suffix_len > 0) TRY(check_ptr(fn, "page_table", page_table, 4));
     TRY(check_ptr(fn, "suffix_len", suffix_len, 4));
     TRY(check_ptr(fn, "out", out, 16));
-    const size_t need = cached8_bytes(D, num_heads, num_kv_heads, num_seqs, L, prefix_len, max_suffix_len);
+    const Cached8Plan p = cached8_plan(D, num_heads, num_kv_heads, num_seqs, L, prefix_len, max_suffix_len);
+    const bool joins = p.prefix_splits + p.suffix_splits > 1;            // else the rows go straight to `out`
+    const size_t need = joins ? cached8_bytes(D, num_heads, num_kv_heads, num_seqs, L, prefix_len, max_suffix_len) : 0;
     TRY(check_workspace(fn, workspace, workspace_bytes, need, 16));
     hipStream_t s = static_cast<hipStream_t>(stream);
     const RangeCheck ranges[] = {
@@ -604,7 +605,6 @@ int lfm2sc_attn_cached8(int dtype, int format, int D, int num_heads, int num_kv_
     c.page_table = page_table; c.max_pages = max_pages; c.suffix_len = suffix_len;
     c.scale = scale;
     c.out = static_cast<uint16_t*>(out); c.out_stride = out_stride;
-    const Cached8Plan p = cached8_plan(D, num_heads, num_kv_heads, num_seqs, L, prefix_len, max_suffix_len);
     const size_t rows = (size_t)num_seqs * (size_t)L * (size_t)num_heads * (size_t)(p.prefix_splits + p.suffix_splits);
     c.part_o = static_cast<float*>(workspace);
     c.part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + round_up(rows * (size_t)D * 4));

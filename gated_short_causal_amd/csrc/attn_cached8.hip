@@ -6,6 +6,12 @@
 
 namespace lfm2sc {
 
+// What the plan's splits go by, and the workspace's bound with them.
+constexpr int kFewTiles = 16, kFewBlocks = 512;          // direct at up to so many tiles and row blocks, whatever else
+constexpr int kMostOwnSplits = 32;
+constexpr int kUnits16 = 2048, kUnits16Shared = 4096, kUnits32 = 1024;      // units of suffixes, by rows of a unit
+constexpr int kCUs = 256;
+
 Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_suffix) {
     Cached8Plan p;
     const int G = Hq / Hkv, rows_unit = 16 * cached8_row_tiles(L, G);
@@ -20,10 +26,10 @@ Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, i
     // 11.3; 32 x 4000 17.6 and 19.3; 64 x 4000 30.6 and 29.7; 128 x 2000 28.3 and 31.5; 256 x 2000 equal; 8 x 8000 23.9 and 16.7.
     // Rows in blocks of 32 (8 tokens of 5 heads of 128): 16 x 4000 34.6 and 41.7, 64 x 999 52 and 36.  Behind a prefix (32
     // sequences, 4096 + 600): 15.9 and 12.1.
-    const int64_t few = base < 128 ? 16 : base < 256 || base > 512 || ptiles > 0 ? 32 : 64;
+    const int64_t few = base < 128 ? kFewTiles : base < 256 || base > 512 || ptiles > 0 ? 32 : 64;
     // Shared: 128 query rows a workgroup.  Shared and split, rows behind 4096 + 600 keys: 64 rows 12.2 and 9.5 us, 256 rows 17.7
     // and 17.3, 1024 rows 33 and 38; behind 16384 + 100: 128 rows 24.4 and 22.5, 160 rows 26.5 and 27.5, 256 rows 29 and 37.
-    if (base <= (ptiles > 0 || rows_unit == 32 ? 512 : 1024) && ptiles + otiles <= few) p.form = kDirect8;
+    if (base <= (ptiles > 0 || rows_unit == 32 ? kFewBlocks : 1024) && ptiles + otiles <= few) p.form = kDirect8;
     else p.form = prefix_len > 0 && rows > kSharedRows ? kShared8 : kSplit8;
     if (p.form == kDirect8) {
         p.suffix_splits = 0;
@@ -41,7 +47,7 @@ Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, i
         const double product = 4. * rows * Hkv * D * prefix_len / 8e14, read = (double)N * max_suffix * Hkv * D / 5e12;
         const double share = product / (product + read);
         const int per_cu = p.form == kSplit8 ? 1 : share > 0.8 ? form_per_simd(D, 1, kShared8) : share > (rows_unit == 32 ? 0.7 : 0.55) ? 2 : 1;
-        const double slots = 256. * per_cu;
+        const double slots = (double)kCUs * per_cu;
         const int64_t want = (int64_t)(slots / (double)(row_blocks * Hkv)), most = (ptiles + 3) / 4;
         const int64_t splits = want < 1 ? 1 : want < most ? want : most;
         const int64_t per = (ptiles + splits - 1) / splits;
@@ -51,13 +57,32 @@ Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, i
     }
     // Suffixes are split, down to 4 tiles, up to 2048 units of a workgroup; of 32 rows up to 1024 (64 x 8 tokens, 999 keys, no
     // prefix: 36 us, with 2048 53), of the shared form, a wave each, up to 4096 (1024 rows behind 4096 + 2000: 75 us, with 2048 80).
-    const int64_t units = rows_unit == 32 ? 1024 : p.form == kShared8 ? 4096 : 2048;
-    const int64_t most = (otiles + 3) / 4, want = std::min<int64_t>(units / base, 32);
+    const int64_t units = rows_unit == 32 ? kUnits32 : p.form == kShared8 ? kUnits16Shared : kUnits16;
+    const int64_t most = (otiles + 3) / 4, want = std::min<int64_t>(units / base, kMostOwnSplits);
     p.suffix_splits = (int)(want < 1 ? 1 : want < most ? want : most);
     if (p.suffix_splits < 1) p.suffix_splits = 1;
     const int per_wg = form_waves(p.form) / own_waves(p.form);
     p.suffix_blocks = (base * p.suffix_splits + per_wg - 1) / per_wg;
     return p;
+}
+
+// At least the rows times parts that any call of these heads with no larger N, L, prefix_len and max_suffix joins, 0 where
+// none joins: the plan's own number falls where a larger batch gets fewer splits or a longer bound another form, and a
+// workspace is taken once for the largest of a program's calls.  Splits of the prefix times query rows are at most
+// the slots times the 128 rows of a workgroup (32 of the split form), splits of the suffixes times rows at most the units
+// times their rows; either is at least 1 where anything is joined, and at most a part to 4 tiles.
+int64_t cached8_part_rows(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_suffix) {
+    const int G = Hq / Hkv, rows_unit = 16 * cached8_row_tiles(L, G);
+    const int64_t rows = (int64_t)N * L * Hq;
+    const int64_t base = (int64_t)N * (((int64_t)L * G + rows_unit - 1) / rows_unit) * Hkv;
+    const int64_t ptiles = ((int64_t)prefix_len + kC8Tile - 1) / kC8Tile, otiles = ((int64_t)max_suffix + kC8Tile - 1) / kC8Tile;
+    const int64_t own = std::min<int64_t>((otiles + 3) / 4, kMostOwnSplits);
+    if (base <= kFewBlocks && ptiles + otiles <= kFewTiles) return 0;        // direct, as are all below it
+    static_assert(16 * kUnits16 == 32 * kUnits32, "both row units");
+    if (prefix_len == 0) return own <= 1 ? 0 : std::min<int64_t>(rows * own, 16 * kUnits16);
+    const int64_t slots = (int64_t)kCUs * std::max(2, form_per_simd(D, 1, kShared8));
+    return std::max(rows, std::min<int64_t>(rows * ((ptiles + 3) / 4), kSharedRows * slots)) +
+           std::max(rows, std::min<int64_t>(rows * own, 16 * kUnits16Shared));
 }
 
 hipError_t launch_attn_cached8(Cached8Args a, int D, bool int8, hipStream_t s) {

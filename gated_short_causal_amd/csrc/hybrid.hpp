@@ -122,6 +122,7 @@ struct Cached8Plan {
     int64_t prefix_blocks, suffix_blocks;
 };
 Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_suffix);
+int64_t cached8_part_rows(int D, int Hq, int Hkv, int N, int L, int prefix_len, int max_suffix);
 
 // Host check of int32 device data (check.hip): n entries within [lo, hi].  With
 // `len`, the entries are runs of `row`, of which run i uses the first

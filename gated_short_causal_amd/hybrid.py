@@ -344,6 +344,7 @@ def lfm2sc_cache8_read(k_pages, v_pages, k_scales, v_scales, page_table, seq_len
 
 
 def lfm2sc_attn_cached8_workspace_bytes(dtype, D, num_heads, num_kv_heads, num_seqs, L, prefix_len, max_suffix_len) -> int:
+    """Never less for larger sizes: asked for with a program's largest, it serves all of its calls with the same heads."""
     code = binding._DTYPES[dtype] if isinstance(dtype, torch.dtype) else int(dtype)
     return int(_lib.hybrid_lib().lfm2sc_attn_cached8_workspace_bytes(code, D, num_heads, num_kv_heads, num_seqs, L, prefix_len,
                                                                      max_suffix_len))

@@ -305,7 +305,10 @@ int lfm2sc_cache8_read(int dtype, int format, int D, int num_kv_heads,
 
 /*
  * Bytes of workspace lfm2sc_attn_cached8 needs; 0 for invalid sizes, when num_seqs or L
- * is 0, and for calls that need none (few keys; many rows without a prefix).
+ * is 0, and where no call up to these sizes needs any (few keys).  Never less for a
+ * larger num_seqs, L, prefix_len or max_suffix_len: a workspace taken for the largest
+ * of a program's calls serves all of them (same D and heads).  A call that joins
+ * nothing takes a NULL workspace too.
  */
 size_t lfm2sc_attn_cached8_workspace_bytes(int dtype, int D, int num_heads, int num_kv_heads, int num_seqs, int L,
                                            int prefix_len, int max_suffix_len);
