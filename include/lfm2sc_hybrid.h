@@ -100,6 +100,8 @@ int lfm2sc_attn_backward(int dtype, int D, int num_heads, int num_kv_heads,
 /*
  * Bytes of workspace lfm2sc_attn_cached needs; 0 for invalid sizes, when num_seqs
  * or L is 0, and for few keys, which need none (workspace may then be NULL).
+ * It goes by the call's own splits, so fewer sequences or pages may need more: ask for
+ * each of the sizes that a program uses.
  */
 size_t lfm2sc_attn_cached_workspace_bytes(int dtype, int D, int num_heads, int num_kv_heads, int num_seqs, int L,
                                           int prefix_len, int max_pages, int page_size);
@@ -276,9 +278,15 @@ enum { LFM2SC_CACHE_E4M3 = 0, LFM2SC_CACHE_INT8 = 1 };
  * times the lowest power of two >= 1 that holds the rows (codes up to 127.5 before
  * rounding, or 448), and the earlier codes are rounded again in steps of the new one,
  * so that a value stays within one step, however many rows follow.  (An old scale of
- * 0 or below 2^-100, or 2^40 times too small, makes a new one and zeros of the earlier codes.)
- * A code is x * (1 / s) rounded to nearest even; beyond the largest it is the largest
- * (infinities too), a NaN is NaN (E4M3) or 0 (INT8).
+ * 0, below 2^-100 or not finite, or 2^40 times too small, makes a new one and zeros of
+ * the earlier codes; an E4M3 NaN among them stays NaN.)
+ * A code is x * (1 / s) rounded to nearest even, 0 where s is 0; beyond the largest it
+ * is the largest (infinities too), a NaN, or an infinity where s is 0, is NaN (E4M3) or
+ * 0 (INT8).
+ * Taking rows back (a smaller seq_len in the next call, as after rejected drafts) does
+ * not undo what they did to a block that keeps earlier tokens: its scale stays as they
+ * made it, and the earlier codes as rounded to it.  Later values of the block then
+ * depend on the rows taken back; the bound of one step holds, a step being that scale's.
  * In the blocks that the call touches, codes of tokens from seq_len on are not values
  * of anything; they keep their bits, and tell nothing under a new scale.
  */
