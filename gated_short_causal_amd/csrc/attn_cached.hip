@@ -512,27 +512,28 @@ CachedPlan cached_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, int
     return p;
 }
 
+int64_t join_blocks(const CachedArgs& a) { return ((int64_t)a.N * a.L * a.Hq + 3) / 4; }
+
 hipError_t launch_attn_join(const CachedArgs& a, int D, hipStream_t s) {
-    const int64_t joins = ((int64_t)a.N * a.L * a.Hq + 3) / 4;
-    if (too_many(joins, 256)) return hipErrorInvalidConfiguration;
-    if (D == 64) hipLaunchKernelGGL((attn_join_kernel<64>), dim3((uint32_t)joins), dim3(256), 0, s, a);
-    else hipLaunchKernelGGL((attn_join_kernel<128>), dim3((uint32_t)joins), dim3(256), 0, s, a);
+    const int64_t blocks = join_blocks(a);
+    if (too_many(blocks, 256)) return hipErrorInvalidConfiguration;
+    if (D == 64) hipLaunchKernelGGL((attn_join_kernel<64>), dim3((uint32_t)blocks), dim3(256), 0, s, a);
+    else hipLaunchKernelGGL((attn_join_kernel<128>), dim3((uint32_t)blocks), dim3(256), 0, s, a);
     return hipGetLastError();
 }
 
 template <int D>
 static hipError_t launch_cached(const CachedArgs& a, const CachedPlan& p, hipStream_t s) {
     const int64_t blocks = p.prefix_blocks + p.suffix_blocks;
-    const int64_t joins = p.prefix_splits + p.suffix_splits > 1 ? ((int64_t)a.N * a.L * a.Hq + 3) / 4 : 0;
-    if (too_many(blocks, 64 * (p.direct ? kDirectW : kCW)) || too_many(joins, 256)) return hipErrorInvalidConfiguration;
+    const bool join = p.prefix_splits + p.suffix_splits > 1;
+    if (too_many(blocks, 64 * (p.direct ? kDirectW : kCW)) || (join && too_many(join_blocks(a), 256))) return hipErrorInvalidConfiguration;
     if (p.direct) {
         hipLaunchKernelGGL((attn_cached_direct_kernel<D>), dim3((uint32_t)blocks), dim3(64 * kDirectW), 0, s, a);
         return hipGetLastError();
     }
     hipLaunchKernelGGL((attn_cached_kernel<D>), dim3((uint32_t)blocks), dim3(64 * kCW), 0, s, a);
-    if (joins > 0)
-        hipLaunchKernelGGL((attn_join_kernel<D>), dim3((uint32_t)joins), dim3(256), 0, s, a);
-    return hipGetLastError();
+    const hipError_t e = hipGetLastError();
+    return e != hipSuccess || !join ? e : launch_attn_join(a, D, s);
 }
 
 hipError_t launch_attn_cached(CachedArgs a, int D, hipStream_t s) {

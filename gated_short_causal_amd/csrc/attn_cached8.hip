@@ -94,7 +94,7 @@ hipError_t launch_attn_cached8(Cached8Args a, int D, bool int8, hipStream_t s) {
     c.suffix_splits = p.suffix_splits;
     const int64_t blocks = p.prefix_blocks + p.suffix_blocks;
     const bool join = p.prefix_splits + p.suffix_splits > 1;
-    if (too_many(blocks, 64 * form_waves(p.form)) || (join && too_many(((int64_t)c.N * c.L * c.Hq + 3) / 4, 256)))
+    if (too_many(blocks, 64 * form_waves(p.form)) || (join && too_many(join_blocks(c), 256)))
         return hipErrorInvalidConfiguration;
     const hipError_t e = D == 64 ? (int8 ? launch_cached8<64, true>(a, p.form, blocks, s) : launch_cached8<64, false>(a, p.form, blocks, s))
                                  : (int8 ? launch_cached8<128, true>(a, p.form, blocks, s) : launch_cached8<128, false>(a, p.form, blocks, s));

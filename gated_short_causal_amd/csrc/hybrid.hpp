@@ -143,6 +143,7 @@ hipError_t launch_attn_prefill(const AttnArgs& a, int D, hipStream_t s);
 int attn_backward_splits(int Hq, int Hkv, int64_t total_T, int N);
 hipError_t launch_attn_backward(const AttnGradArgs& a, int D, hipStream_t s);
 hipError_t launch_attn_cached(CachedArgs a, int D, hipStream_t s);
+int64_t join_blocks(const CachedArgs& a);         // workgroups of it
 hipError_t launch_attn_join(const CachedArgs& a, int D, hipStream_t s);
 hipError_t launch_cache8(Cache8Args a, int D, bool int8, bool f32, bool write, hipStream_t s);
 hipError_t launch_attn_cached8(Cached8Args a, int D, bool int8, hipStream_t s);
