@@ -43,7 +43,10 @@ Cached8Plan cached8_plan(int D, int Hq, int Hkv, int N, int L, int prefix_len, i
         // in between wait for the CUs that have one more.  256 and 512 workgroups, us: 32 x 4 rows of 5 heads of 128, 4096 + 999
         // (share .67) 32.6 and 40.2; 64 x 8, 2048 + 999 (.67) 69.7 and 76.3; 1024 rows of 64, 8192 + 600 (.58) 51.8 and 48.7;
         // 16384 + 600 (.73) 90.7 and 67.7.  2048 rows, 2048 + 600 (.25): 256 56 us, 128 65; 1024 rows, 4096 + 600 (.4): 256
-        // 34, 192 39, 320 38.
+        // 34, 192 39, 320 38.  The number of splits is rounded down, so a batch just past a divisor of the slots leaves many
+        // empty and walks longer parts: 512 single tokens behind 8192 + 1000 keys 116 us, 520 of them 191 (102 and 103 x 8
+        // behind 4096 + 999, 5 heads of 128: 146 and 145).  The points are of block scales, those of D = 64 of single tokens;
+        // the forms of 32 rows and a scale a token go by the same rule.
         const double product = 4. * rows * Hkv * D * prefix_len / 8e14, read = (double)N * max_suffix * Hkv * D / 5e12;
         const double share = product / (product + read);
         const int per_cu = p.form == kSplit8 ? 1 : share > 0.8 ? form_per_simd(D, 1, kShared8) : share > (rows_unit == 32 ? 0.7 : 0.55) ? 2 : 1;

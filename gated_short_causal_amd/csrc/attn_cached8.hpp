@@ -18,7 +18,8 @@
 // its A operand the lane needs 16 neighbouring tokens of a channel: one 16-byte
 // load of the V page.  K's k order is free as well: lane g takes bytes
 // [D / 4 g, D / 4 (g + 1)) of a key's codes, and the query's operand the same.
-// Nothing but the waves' join goes through LDS.
+// Where a wave reads tiles for its own rows, nothing but the waves' join goes through
+// LDS; a prefix of many rows is staged there as operands (shared8).
 //
 // Measured (one MI355X, device time): 64 sequences of up to 16384 keys, 24/8 heads of
 // 128, a scale a token: 212 us for 1.13 GB, 5.3 TB/s (1 GiB copies reach 5.1): reads
@@ -100,8 +101,8 @@ struct Keys8 {
 // page is uniform (0 in pages of up to 64 tokens), and a lane's 16 tokens lie at the
 // same distance from it in every tile: an address is a constant of the lane, one
 // product with a page number and the uniform offset.  No branch on the page size:
-// the loads in flight are then counted exactly.  Tokens past the end are read from
-// the last page that exists.
+// the loads in flight are then counted exactly, unless the form spills registers
+// (form_per_simd).  Tokens past the end are read from the last page that exists.
 template <int D, bool kToken>
 struct Loader8 {
     const Cached8Args& a;
@@ -275,8 +276,11 @@ __device__ __forceinline__ void refer8(Rows8<D, NT>& r, const float (&mn)[NT]) {
 }
 
 // Then the scores of block b become probabilities times their values' scales, words
-// 2 (b & 1) and + 1 of operand b >> 1 of the second product.  between() runs when
-// the scores have been read.
+// 2 (b & 1) and + 1 of operand b >> 1 of the second product.  They are rounded to
+// bf16 because that is what the matrix unit multiplies: an output is then 1.8e-3 to
+// 2.0e-3 off in the 2-norm, where its own rounding is 1.6e-3; what is left of p as a
+// second operand would double the second product.  between() runs when the scores
+// have been read.
 template <int b, int D, int NT, bool kToken, typename F>
 __device__ __forceinline__ void weigh8(Rows8<D, NT>& r, f32x4 (&s)[NT][4], bf16x8 (&p)[NT][2], const Scales8<kToken>& sc, F between) {
     float x[NT][4];
@@ -664,7 +668,8 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
             clean_v(i + 1);
         }
         // What is done beside the product with V: one part a region.  A register is loaded in a later region than its last
-        // use: in the same one the compiler may load first, into another register, and wait for the load to copy it.
+        // use: in the same one the compiler may load first, into another register, and wait for the load to copy it.  (Where
+        // it spills an address instead, form_per_simd, the reload waits for the loads before it all the same.)
         auto part = [&](auto b_c) {
             constexpr int b = decltype(b_c)::value, q = D / 64;      // q regions for each of four parts
             const bool masked = kMore == 1 && end < kC8Tile;
@@ -778,7 +783,12 @@ __device__ __forceinline__ void shared8(const Cached8Args& a, const Keys8& s, in
 //            (1024 rows behind 4096 + 600: 33 us; with a workgroup to a suffix, 54)
 enum Form8 { kDirect8, kSplit8, kShared8 };
 constexpr int form_waves(int form) { return form == kDirect8 ? 8 : 4; }
-// waves a SIMD, which bounds their registers: 128, 168 or 256 of 512
+// waves a SIMD, which bounds their registers: 128, 168 or 256 of 512.  Registers that the compiler spills within that:
+// 16 rows a unit: none for D = 128; D = 64 none direct, 0 or 1 split, shared 2 (block scales) or 9 to 11 (a scale a token);
+// 32 rows: D = 64 none direct, 13 to 21 split, 8 to 23 shared; D = 128 1 to 7 direct, 13 to 23 split, 4 to 8 shared.
+// A spilled address is reloaded in the loop, and as a wave's memory operations are waited for in order, the wait covers
+// the tile's loads too: part of why 256 tokens behind 4096 + 600 keys take 38 us with block scales and 53 with a scale a
+// token (64 x 8 behind 16384 + 999, 32 / 8 heads of 64: 114 to 122 and 160).
 constexpr int form_per_simd(int D, int NT, int form) {
     if (D == 128) return 2;
     if (form == kSplit8) return NT == 1 ? 4 : 3;

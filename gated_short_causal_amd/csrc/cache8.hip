@@ -13,13 +13,17 @@
 // on a virtual axis it begins at cu[i] / U + 2 i, so units [0, T / U + 2 N) hold
 // every sequence's, and a wave finds its own by a search over that monotone key.
 //
-// Measured (one MI355X): 65536 tokens of 8 heads of 128 written in 86 us (4.7 TB/s of
-// rows, codes and scales; copies reach 5.1; vector unit 38% busy), read back in 65 us.  8 x
-// <= 2048 tokens of 64: 9.9 and 6.7 us.  64 x 8 drafted tokens: 9.1 and 9.5; 256 single
-// tokens 5.9, the block that each joins 8.5: four dependent reads of about 1 us each
-// (lengths, page number, codes and scales beside rows), not bytes.  With a wave for K and
-// one for V, and earlier codes asked for after the scales: 14.4 us (64 x 8 written), 7.3
-// (256), 12.7 (8 x 2048).
+// Measured (one MI355X): 65536 tokens of 8 heads of 128 written in 80 to 86 us (4.7 TB/s of
+// rows, codes and scales; copies reach 5.1; vector unit 38% busy), read back in 65 us
+// behind the write, when part of the codes is in the last cache, else in 75 us, and in 93
+// to 108 into columns of one buffer; fp32 rows 131 and, into such columns, 176 us (130 at
+// the copy's rate).  8 x <= 2048 tokens of 64: 9.9 and 6.7 us; 8 x 1024 with a scale a
+// token 10.5 and 7.1 us (fp32 11.9 and 10.6), a scale for 16 tokens 8.4 and 6.9 (10.3 and
+// 11.0): a wave's loads, maxima over lanes and stores follow each other, in one round of
+// the card.  64 x 8 drafted tokens: 9.1 and 9.5; 256 single tokens 4.9 to 5.9, the block
+// that each joins 8.5: four dependent reads of about 1 us each (lengths, page number,
+// codes and scales beside rows), not bytes.  With a wave for K and one for V, and earlier
+// codes asked for after the scales: 14.4 us (64 x 8 written), 7.3 (256), 12.7 (8 x 2048).
 #include "attn_common.hpp"
 #include "cache8.hpp"
 #include "seq_find.hpp"

@@ -6,9 +6,10 @@
 //   V page  [Hkv][S / 16][D][16]  a channel's codes of 16 tokens are 16 bytes
 // A head's 16 tokens are 16 D contiguous bytes in both.  V lies as the matrix
 // unit takes it in the product with the probabilities (a channel, and tokens in
-// a row), so the attention loads both straight into registers: no LDS, no
-// transposing read.  Scales [Hkv][S / scale_tokens] fp32 a page, a value is its
-// code times the scale of its block of tokens.
+// a row), so the attention loads both straight into registers, with no transposing
+// read (and through LDS only where many rows share a tile).  Scales
+// [Hkv][S / scale_tokens] fp32 a page, a value is its code times the scale of its
+// block of tokens.
 #pragma once
 
 #include "common.hpp"
